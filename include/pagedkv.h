@@ -82,6 +82,7 @@ typedef struct {
 #define PA_DEVERR_SLOT 4        /* a slot >= num_blocks * block_size */
 #define PA_DEVERR_TIMEOUT 8     /* a bounded wait on a shared-memory copy ran out */
 #define PA_DEVERR_COPY_PAIR 16  /* a copy pair id outside [0, num_blocks) */
+#define PA_DEVERR_TREE 32       /* bad tree offsets, parent, or accepted path */
 
 /* pa_write_kv - store the K and V of new tokens in their cache slots.
  *
@@ -285,6 +286,149 @@ pa_status pa_swap_blocks(void *const *src_key_caches, void *const *src_value_cac
                          void *const *dst_value_caches, const pa_cache_desc *dst,
                          int32_t num_layers, const int64_t *block_mapping, int32_t num_pairs,
                          int32_t *dev_err, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Trees of drafted tokens
+ *
+ * A speculative step drafts several tokens behind each running sequence,
+ * arranged as a tree (a chain is a tree), runs the model once over all of
+ * them, and keeps the path that the model agrees with. The decode calls above
+ * take one query token per sequence; these take every node of every tree:
+ *
+ *   pa_tree_mask     parents -> ancestor bits and depths, once a step
+ *   pa_write_kv      each layer: the nodes' K/V into their slots
+ *   pa_tree_decode   each layer: attention of every node
+ *   pa_tree_accept   the kept path of each tree
+ *   pa_tree_compact  the kept nodes' K/V rows moved behind the context, all
+ *                    layers at once
+ *
+ * (pa_bm_prepare_tree and pa_bm_truncate do the block manager's share.)
+ *
+ * Trees are packed: sequence s has the nodes tree_start[s] ..
+ * tree_start[s+1] - 1 of every per-node array (tree_start is device int32
+ * [num_seqs + 1], not decreasing, tree_start[0] >= 0). A tree may be empty.
+ * Node i of a tree is named by its index i within the tree; its K/V lie at
+ * position context_lens[s] + i of the sequence, where context_lens[s] counts
+ * the tokens cached before the tree. A node's parent comes before it.
+ * Per-node arrays have num_tokens rows; rows that belong to no tree (padding
+ * behind the last one, or before tree_start[0]) are neither read nor
+ * written. Offsets that decrease or leave [0, num_tokens], and trees of more
+ * nodes than the call's limit, set PA_DEVERR_TREE; that sequence is then
+ * skipped (its outputs are left as they were, unless the call says
+ * otherwise).
+ * ------------------------------------------------------------------------- */
+#define PA_TREE_MAX_NODES 1024 /* nodes of one tree */
+
+/* pa_tree_mask - the ancestor bits and depths of every node.
+ *
+ * parents     device int32 [num_tokens]: the index within its tree of each
+ *             node's parent, -1 for a root (a tree may have several). A
+ *             parent that is not below the node's own index sets
+ *             PA_DEVERR_TREE and counts as -1.
+ * mask        device int32 [num_tokens][mask_words]: bit j % 32 of word
+ *             j / 32 is set when node j is the node itself or an ancestor of
+ *             it; every other bit of the row is cleared.
+ * depth       device int32 [num_tokens] or NULL: ancestors of each node, so
+ *             that context_len + depth is its position in the text.
+ * mask_words  words of a row, 1 .. PA_TREE_MAX_NODES / 32; the limit on a
+ *             tree's nodes is 32 * mask_words.
+ */
+pa_status pa_tree_mask(int32_t *mask, int32_t *depth, const int32_t *parents,
+                       const int32_t *tree_start, int32_t num_seqs, int32_t num_tokens,
+                       int32_t mask_words, int32_t *dev_err, void *stream);
+
+/* Bytes of workspace pa_tree_decode needs on the current device, for any
+ * batch over caches of this shape; (size_t)-1 on invalid arguments. The
+ * workspace needs no initialisation and keeps nothing between calls. */
+size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
+
+/* pa_tree_decode - attention of every node of every tree: for node i of
+ * sequence s and head h, out = softmax(scale * q K^T) V over the
+ * context_lens[s] cached tokens and those nodes j of its own tree whose bit
+ * is set in its mask row, all reached through the block table.
+ *
+ * out         device [num_tokens][num_heads][head_dim] of out_dtype.
+ * query       device [num_tokens][num_heads][head_dim], cache dtype (fp8
+ *             caches: the descriptor's io_dtype), 16-byte aligned. The group
+ *             size num_heads / num_kv_heads is at most 128.
+ * block_tables, max_blocks_per_seq  as for pa_decode; the first
+ *             ceil((context_len + nodes) / block_size) entries of a row are
+ *             read, for sequences whose tree is not empty.
+ * context_lens  device int32 [num_seqs], without the tree. A negative
+ *             one, or one whose tree does not fit the table, sets
+ *             PA_DEVERR_CONTEXT_LEN and makes the rows of that tree NaN.
+ * mask        device int32 [num_tokens][mask_words], as pa_tree_mask writes
+ *             it; any bits are allowed (bit j of row i: node i attends to
+ *             node j), those at or past the tree's end count for nothing. A
+ *             row with no cached token and no bit gives a zero output row.
+ *             What a node does not attend to cannot reach its output, NaN
+ *             and infinities included.
+ * workspace   device, >= pa_tree_decode_workspace_size(cache) bytes, 16-byte
+ *             aligned. Two calls sharing one workspace on different streams
+ *             race.
+ * Nothing about the lengths is needed on the host: the work is divided on
+ * the device, so a captured call can be replayed with other lengths.
+ * Precision: products and sums, the softmax and the P.V sums are fp32, the
+ * weight p of the P.V products is rounded to the row type (fp8 caches: the
+ * io_dtype) first, and the output once, to out_dtype. A block id outside the
+ * pool sets PA_DEVERR_BLOCK_ID and makes that sequence's output NaN.
+ */
+pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,
+                         int32_t num_tokens, int32_t num_heads, const void *key_cache,
+                         const void *value_cache, const pa_cache_desc *cache,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, const int32_t *tree_start,
+                         const int32_t *mask, int32_t mask_words, float scale, void *workspace,
+                         size_t workspace_bytes, int32_t *dev_err, void *stream);
+
+/* pa_tree_accept - the path of each tree that the model agrees with.
+ *
+ * Starting at node 0 (the token every drafted one follows), the path goes on
+ * to the lowest child whose drafted token is the token the model picked at
+ * the current node, while there is one and the path has fewer than max_path
+ * nodes. With target_tokens picked greedily this is greedy verification;
+ * with target_tokens sampled from the model's distribution at each node the
+ * kept tokens are distributed as if sampled one by one.
+ *
+ * accepted       device int32 [num_seqs][max_path]: the path's nodes, -1 past
+ *                its end. 1 <= max_path <= PA_TREE_MAX_NODES.
+ * accepted_lens  device int32 [num_seqs]: nodes of the path (0 for an empty
+ *                tree, else at least 1).
+ * next_token     device int64 [num_seqs]: the model's token at the path's
+ *                last node, -1 for an empty tree.
+ * parents        as for pa_tree_mask (a bad one counts as -1).
+ * draft_tokens, target_tokens  device int64 [num_tokens]: each node's own
+ *                token, and the token the model picked after it.
+ * A tree of more than PA_TREE_MAX_NODES nodes (or bad offsets) gives the
+ * results of an empty one. */
+pa_status pa_tree_accept(int32_t *accepted, int32_t *accepted_lens, int64_t *next_token,
+                         const int32_t *parents, const int32_t *tree_start,
+                         const int64_t *draft_tokens, const int64_t *target_tokens,
+                         int32_t num_seqs, int32_t num_tokens, int32_t max_path,
+                         int32_t *dev_err, void *stream);
+
+/* pa_tree_compact - move the kept nodes' K/V rows to the positions that
+ * follow the context: for k < accepted_lens[s], the row at position
+ * context_lens[s] + accepted[s][k] goes to position context_lens[s] + k, in
+ * both caches of every layer, in place.
+ *
+ * key_caches, value_caches  HOST arrays of num_layers device pointers, as for
+ *                pa_copy_blocks.
+ * context_lens   device int32 [num_seqs], without the tree.
+ * accepted, accepted_lens  device, as pa_tree_accept writes them: each path
+ *                ascending. A length outside [0, max_path], a negative node
+ *                or a path that does not ascend sets PA_DEVERR_TREE and the
+ *                sequence is skipped; a position past the table sets
+ *                PA_DEVERR_CONTEXT_LEN and skips it too. A block id outside
+ *                the pool sets PA_DEVERR_BLOCK_ID and that row is skipped.
+ * The blocks that hold the trees belong to one sequence each (copy-on-write
+ * has run). num_seqs <= 65535. */
+pa_status pa_tree_compact(void *const *key_caches, void *const *value_caches,
+                          int32_t num_layers, const pa_cache_desc *cache,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, const int32_t *accepted,
+                          const int32_t *accepted_lens, int32_t num_seqs, int32_t max_path,
+                          int32_t *dev_err, void *stream);
 
 /* Self-test of failure detection: one warp waits on a shared-memory barrier
  * that nothing will complete, through the same bounded wait every kernel

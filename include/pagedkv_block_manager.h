@@ -89,6 +89,27 @@ pa_status pa_bm_prepare_decode(pa_block_manager *bm, const int64_t *seqs, int32_
                                int32_t *context_lens, int64_t *slot_mapping,
                                int64_t *copy_pairs, int32_t *num_pairs);
 
+/* One step over drafted trees for n sequences: reserve tree_sizes[i] (>= 0)
+ * slots behind each (in the order given) and fill the step's inputs.
+ *   block_tables   host int32 [n][max_blocks_per_seq], -1 past each table
+ *   context_lens   host int32 [n], tokens before the tree
+ *   tree_start     host int32 [n + 1], offsets of the packed nodes
+ *   slot_mapping   host int64 [sum of tree_sizes], slot of each node
+ *   copy_pairs     host int64 [n][2], (src, dst) to copy before writing (a
+ *                  shared last block that a tree would write into);
+ *                  *num_pairs receives how many were filled
+ * Checks first, as pa_bm_prepare_decode does, and fails without change. The
+ * sequence holds its whole tree afterwards: pa_bm_truncate drops what was not
+ * kept once pa_tree_compact has moved what was. */
+pa_status pa_bm_prepare_tree(pa_block_manager *bm, const int64_t *seqs, int32_t n,
+                             const int32_t *tree_sizes, int32_t max_blocks_per_seq,
+                             int32_t *block_tables, int32_t *context_lens,
+                             int32_t *tree_start, int64_t *slot_mapping, int64_t *copy_pairs,
+                             int32_t *num_pairs);
+/* Keep the first `tokens` tokens of seq (0 <= tokens <= what it holds) and
+ * return the blocks past them. */
+pa_status pa_bm_truncate(pa_block_manager *bm, int64_t seq, int32_t tokens);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,7 @@ Cache tensors are [num_blocks, num_heads, block_size, head_dim] fp16/bf16
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,6 +34,8 @@ PA_DEVERR_CONTEXT_LEN = 2
 PA_DEVERR_SLOT = 4
 PA_DEVERR_TIMEOUT = 8
 PA_DEVERR_COPY_PAIR = 16
+PA_DEVERR_TREE = 32
+PA_TREE_MAX_NODES = 1024
 PA_MAX_LAYERS = 256
 
 _DTYPE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
@@ -115,6 +118,20 @@ _lib.pa_swap_blocks.restype = ctypes.c_int
 _lib.pa_swap_blocks.argtypes = [ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(CacheDesc),
                                 ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(CacheDesc),
                                 _i32, _P, _i32, _P, _P]
+_lib.pa_tree_mask.restype = ctypes.c_int
+_lib.pa_tree_mask.argtypes = [_P, _P, _P, _P, _i32, _i32, _i32, _P, _P]
+_lib.pa_tree_decode_workspace_size.restype = ctypes.c_size_t
+_lib.pa_tree_decode_workspace_size.argtypes = [ctypes.POINTER(CacheDesc)]
+_lib.pa_tree_decode.restype = ctypes.c_int
+_lib.pa_tree_decode.argtypes = [_P, ctypes.c_int, _P, _i32, _i32, _i32, _P, _P,
+                                ctypes.POINTER(CacheDesc), _P, _i32, _P, _P, _P, _i32,
+                                ctypes.c_float, _P, ctypes.c_size_t, _P, _P]
+_lib.pa_tree_accept.restype = ctypes.c_int
+_lib.pa_tree_accept.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _P, _P]
+_lib.pa_tree_compact.restype = ctypes.c_int
+_lib.pa_tree_compact.argtypes = [ctypes.POINTER(_P), ctypes.POINTER(_P), _i32,
+                                 ctypes.POINTER(CacheDesc), _P, _i32, _P, _P, _P, _i32, _i32, _P,
+                                 _P]
 _lib.pa_selftest_wait_timeout.restype = ctypes.c_int
 _lib.pa_selftest_wait_timeout.argtypes = [_P, ctypes.c_uint32, _P]
 _lib.pa_status_string.restype = ctypes.c_char_p
@@ -374,6 +391,187 @@ def swap_blocks(src_key_caches, src_value_caches, dst_key_caches, dst_value_cach
     _check(_lib.pa_swap_blocks(arr(src_key_caches), arr(src_value_caches), ctypes.byref(sd),
                                arr(dst_key_caches), arr(dst_value_caches), ctypes.byref(dd),
                                L, _ptr(block_mapping), n, _ptr(dev_err), stream))
+
+
+def _on_device(device):
+    """Launches go to the current device: the tensors' own, for the call."""
+    if device.index == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return torch.cuda.device(device)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _need_vector(t, name, dtype, size, device):
+    _need(t, name, dtype)
+    if t.dim() != 1 or (size is not None and t.shape[0] != size):
+        raise ValueError(f"{name} must have shape [{'' if size is None else size}]")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _num_trees(tree_start, device):
+    _need_vector(tree_start, "tree_start", torch.int32, None, device)
+    if tree_start.shape[0] < 1:
+        raise ValueError("tree_start must have one entry more than there are sequences")
+    return tree_start.shape[0] - 1
+
+
+def _need_err(dev_err, device):
+    if dev_err is not None:
+        _need(dev_err, "dev_err", torch.int32)
+        if dev_err.numel() < 1 or dev_err.device != device:
+            raise ValueError(f"dev_err must be an int32 word on {device}")
+
+
+def tree_mask(mask, depth, parents, tree_start, dev_err=None):
+    """Ancestor bits and depths of drafted trees: ``parents`` int32 [N] (-1:
+    a root) and ``tree_start`` int32 [S + 1] give ``mask`` int32 [N, W] (bit
+    j % 32 of word j // 32: node j is the row's node or an ancestor of it)
+    and ``depth`` int32 [N] (or None). Trees have at most 32 * W nodes. Rows
+    of no tree are left as they were."""
+    _need(parents, "parents", torch.int32)
+    dev, N = parents.device, parents.numel()
+    _need_vector(parents, "parents", torch.int32, None, dev)
+    S = _num_trees(tree_start, dev)
+    _need(mask, "mask", torch.int32)
+    if mask.dim() != 2 or mask.shape[0] != N or mask.device != dev:
+        raise ValueError(f"mask must be [{N}, words] on {dev}")
+    if depth is not None:
+        _need_vector(depth, "depth", torch.int32, N, dev)
+    _need_err(dev_err, dev)
+    with _on_device(dev):
+        _check(_lib.pa_tree_mask(_ptr(mask), _ptr(depth), _ptr(parents), _ptr(tree_start), S, N,
+                                 mask.shape[1], _ptr(dev_err), _stream(parents)))
+    return mask, depth
+
+
+def tree_decode_workspace_size(cache):
+    """Bytes of workspace :func:`tree_decode` needs on the current device.
+    ``cache``: a key cache (tensor or Fp8Cache) or a CacheDesc."""
+    desc = cache if isinstance(cache, CacheDesc) else cache_desc(cache)
+    n = _lib.pa_tree_decode_workspace_size(ctypes.byref(desc))
+    if n == SIZE_MAX:
+        raise ValueError("invalid arguments to tree_decode_workspace_size")
+    return int(n)
+
+
+def alloc_tree_workspace(cache):
+    """A workspace for :func:`tree_decode` over ``cache`` (and any other cache
+    of its head dimension), on its device. Needs no initialisation."""
+    with _on_device(cache.device):
+        return torch.empty(tree_decode_workspace_size(cache), dtype=torch.uint8,
+                           device=cache.device)
+
+
+def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, tree_start, mask,
+                scale, workspace=None, dev_err=None):
+    """Attention of every node of every drafted tree: ``query`` and ``out``
+    [N, H, D], nodes of sequence s at rows tree_start[s] .. tree_start[s+1]-1.
+    Node i attends to the ``context_lens[s]`` cached tokens and to those nodes
+    j of its own tree whose bit is set in ``mask`` [N, W] (see
+    :func:`tree_mask`); node j's K/V are at position context_lens[s] + j.
+    ``out`` may be fp16, bf16 or fp32; ``workspace`` is allocated here when
+    not given."""
+    _need_cache(key_cache, "key_cache")
+    _need_cache(value_cache, "value_cache", key_cache)
+    _need(query, "query", io_dtype(key_cache))
+    _need(out, "out")
+    if out.dtype not in _DTYPE:
+        raise ValueError("out dtype must be float16, bfloat16 or float32")
+    desc, dev = cache_desc(key_cache), key_cache.device
+    if query.dim() != 3 or out.shape != query.shape or query.shape[2] != desc.head_dim:
+        raise ValueError(f"query and out must be [N, H, {desc.head_dim}]")
+    N, H, _ = query.shape
+    S = _num_trees(tree_start, dev)
+    _need_vector(context_lens, "context_lens", torch.int32, S, dev)
+    _need(block_tables, "block_tables", torch.int32)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError(f"block_tables must be [{S}, blocks]")
+    _need(mask, "mask", torch.int32)
+    if mask.dim() != 2 or mask.shape[0] != N:
+        raise ValueError(f"mask must be [{N}, words]")
+    for t in (value_cache, query, out, block_tables, mask):
+        if t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}")
+    _need_err(dev_err, dev)
+    if workspace is None:
+        workspace = alloc_tree_workspace(key_cache)
+    _need(workspace, "workspace")
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    with _on_device(dev):
+        _check(_lib.pa_tree_decode(_ptr(out), _DTYPE[out.dtype], _ptr(query), S, N, H,
+                                   _ptr(key_cache), _ptr(value_cache), ctypes.byref(desc),
+                                   _ptr(block_tables), block_tables.shape[1],
+                                   _ptr(context_lens), _ptr(tree_start), _ptr(mask),
+                                   mask.shape[1], float(scale), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _ptr(dev_err),
+                                   _stream(query)))
+    return out
+
+
+def tree_accept(accepted, accepted_lens, next_token, parents, tree_start, draft_tokens,
+                target_tokens, dev_err=None):
+    """The path of each tree that the model agrees with: from node 0 on to
+    the lowest child whose token (``draft_tokens`` int64 [N]) is the one the
+    model picked at the node (``target_tokens`` int64 [N]). Writes
+    ``accepted`` int32 [S, max_path] (-1 past the path), ``accepted_lens``
+    int32 [S] and ``next_token`` int64 [S], the model's token at the path's
+    last node. A path is cut at max_path nodes."""
+    _need(parents, "parents", torch.int32)
+    dev, N = parents.device, parents.numel()
+    _need_vector(parents, "parents", torch.int32, None, dev)
+    S = _num_trees(tree_start, dev)
+    _need_vector(draft_tokens, "draft_tokens", torch.int64, N, dev)
+    _need_vector(target_tokens, "target_tokens", torch.int64, N, dev)
+    _need(accepted, "accepted", torch.int32)
+    if accepted.dim() != 2 or accepted.shape[0] != S or accepted.device != dev:
+        raise ValueError(f"accepted must be [{S}, max_path] on {dev}")
+    _need_vector(accepted_lens, "accepted_lens", torch.int32, S, dev)
+    _need_vector(next_token, "next_token", torch.int64, S, dev)
+    _need_err(dev_err, dev)
+    with _on_device(dev):
+        _check(_lib.pa_tree_accept(_ptr(accepted), _ptr(accepted_lens), _ptr(next_token),
+                                   _ptr(parents), _ptr(tree_start), _ptr(draft_tokens),
+                                   _ptr(target_tokens), S, N, accepted.shape[1], _ptr(dev_err),
+                                   _stream(parents)))
+    return accepted, accepted_lens, next_token
+
+
+def tree_compact(key_caches, value_caches, block_tables, context_lens, accepted, accepted_lens,
+                 dev_err=None):
+    """Move the accepted nodes' K/V rows behind the context, in place and in
+    every layer: position context_lens[s] + accepted[s, k] to position
+    context_lens[s] + k for k < accepted_lens[s]."""
+    if len(key_caches) != len(value_caches) or not key_caches:
+        raise ValueError("need the same, non-zero number of K and V caches")
+    like = key_caches[0]
+    dev = like.device
+    for caches in (key_caches, value_caches):
+        for c in caches:
+            _need_cache(c, "cache", like)
+            if c.device != dev:
+                raise ValueError(f"all caches must be on {dev}")
+    desc, L = cache_desc(like), len(key_caches)
+    _need(accepted, "accepted", torch.int32)
+    if accepted.dim() != 2 or accepted.device != dev:
+        raise ValueError(f"accepted must be [sequences, max_path] on {dev}")
+    S = accepted.shape[0]
+    _need_vector(accepted_lens, "accepted_lens", torch.int32, S, dev)
+    _need_vector(context_lens, "context_lens", torch.int32, S, dev)
+    _need(block_tables, "block_tables", torch.int32)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or block_tables.device != dev:
+        raise ValueError(f"block_tables must be [{S}, blocks] on {dev}")
+    _need_err(dev_err, dev)
+    kp = (_P * L)(*[c.data_ptr() for c in key_caches])
+    vp = (_P * L)(*[c.data_ptr() for c in value_caches])
+    with _on_device(dev):
+        _check(_lib.pa_tree_compact(kp, vp, L, ctypes.byref(desc), _ptr(block_tables),
+                                    block_tables.shape[1], _ptr(context_lens), _ptr(accepted),
+                                    _ptr(accepted_lens), S, accepted.shape[1], _ptr(dev_err),
+                                    _stream(like.data if isinstance(like, Fp8Cache) else like)))
 
 
 def selftest_wait_timeout(limit_us: int = 1000, device="cuda") -> int:

@@ -25,7 +25,9 @@ for _n, _a in [("pa_bm_num_free", [_P]), ("pa_bm_can_allocate", [_P, _i32]),
 for _n, _a in [("pa_bm_add_sequence", [_P, _i64]), ("pa_bm_allocate_tokens", [_P, _i64, _i32]),
                ("pa_bm_fork", [_P, _i64, _i64]), ("pa_bm_append_token", [_P, _i64, _P, _P, _P]),
                ("pa_bm_free_sequence", [_P, _i64]),
-               ("pa_bm_prepare_decode", [_P, _P, _i32, _i32, _P, _P, _P, _P, _P])]:
+               ("pa_bm_prepare_decode", [_P, _P, _i32, _i32, _P, _P, _P, _P, _P]),
+               ("pa_bm_prepare_tree", [_P, _P, _i32, _P, _i32, _P, _P, _P, _P, _P, _P]),
+               ("pa_bm_truncate", [_P, _i64, _i32])]:
     getattr(_lib, _n).restype = ctypes.c_int
     getattr(_lib, _n).argtypes = _a
 
@@ -115,3 +117,34 @@ class BlockManager:
                                          pairs.ctypes.data, ctypes.byref(npairs)))
         return {"block_tables": bt, "context_lens": ctx, "slot_mapping": slots,
                 "copy_pairs": pairs[:npairs.value].copy()}
+
+    def prepare_tree(self, seqs, tree_sizes, max_blocks_per_seq: int) -> dict:
+        """Reserve ``tree_sizes[i]`` slots behind each of ``seqs`` and return
+        the step's inputs: block_tables, context_lens (without the trees),
+        tree_start, slot_mapping (one slot per node), copy_pairs."""
+        ids = np.ascontiguousarray(seqs, dtype=np.int64)
+        sizes = np.ascontiguousarray(tree_sizes, dtype=np.int32)
+        n = ids.shape[0]
+        if sizes.shape != (n,):
+            raise ValueError("one tree size per sequence")
+        bt = np.empty((n, max_blocks_per_seq), dtype=np.int32)
+        ctx = np.empty(n, dtype=np.int32)
+        start = np.empty(n + 1, dtype=np.int32)
+        # More nodes than the pool has slots: refused below, whatever room there is.
+        room = min(int(np.maximum(sizes, 0).sum(dtype=np.int64)),
+                   self.num_blocks * self.block_size)
+        slots = np.empty(max(room, 1), dtype=np.int64)
+        pairs = np.empty((max(n, 1), 2), dtype=np.int64)
+        npairs = _i32()
+        _check(_lib.pa_bm_prepare_tree(self._h, ids.ctypes.data, n, sizes.ctypes.data,
+                                       max_blocks_per_seq, bt.ctypes.data, ctx.ctypes.data,
+                                       start.ctypes.data, slots.ctypes.data, pairs.ctypes.data,
+                                       ctypes.byref(npairs)))
+        return {"block_tables": bt, "context_lens": ctx, "tree_start": start,
+                "slot_mapping": slots[:start[n]].copy(),
+                "copy_pairs": pairs[:npairs.value].copy()}
+
+    def truncate(self, seq: int, tokens: int) -> None:
+        """Keep the first ``tokens`` tokens of ``seq``; the blocks past them
+        go back to the pool."""
+        _check(_lib.pa_bm_truncate(self._h, seq, tokens))

@@ -4,6 +4,7 @@
 #include "pagedkv_block_manager.h"
 
 #include <algorithm>
+#include <climits>
 #include <new>
 #include <unordered_map>
 #include <unordered_set>
@@ -275,6 +276,107 @@ pa_status pa_bm_prepare_decode(pa_block_manager *bm, const int64_t *seqs, int32_
     }
     if (num_pairs)
         *num_pairs = pairs;
+    return ok();
+}
+
+pa_status pa_bm_prepare_tree(pa_block_manager *bm, const int64_t *seqs, int32_t n,
+                             const int32_t *tree_sizes, int32_t max_blocks_per_seq,
+                             int32_t *block_tables, int32_t *context_lens,
+                             int32_t *tree_start, int64_t *slot_mapping, int64_t *copy_pairs,
+                             int32_t *num_pairs)
+{
+    if (!bm)
+        return fail(PA_ERR_INVALID_ARG, "NULL block manager");
+    if (n < 0 || max_blocks_per_seq < 1)
+        return fail(PA_ERR_INVALID_ARG, "bad size argument");
+    if (!tree_start ||
+        (n > 0 && (!seqs || !tree_sizes || !block_tables || !context_lens || !copy_pairs)))
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    // The whole step first, as for pa_bm_prepare_decode.
+    // Tables get the room they will need here, so nothing after this can throw.
+    int64_t need = 0, nodes = 0;
+    const int32_t bs = bm->block_size;
+    try {
+        std::unordered_set<int64_t> seen;
+        std::unordered_map<int32_t, int32_t> drops; // ref-count drops from earlier copies
+        for (int32_t i = 0; i < n; ++i) {
+            pa_block_manager::Seq *s = bm->find(seqs[i]);
+            if (!s)
+                return fail(PA_ERR_INVALID_ARG, "unknown sequence %lld", (long long)seqs[i]);
+            if (!seen.insert(seqs[i]).second)
+                return fail(PA_ERR_INVALID_ARG, "sequence %lld twice in one step",
+                            (long long)seqs[i]);
+            const int32_t t = tree_sizes[i];
+            if (t < 0)
+                return fail(PA_ERR_INVALID_ARG, "sequence %lld: tree of %d nodes",
+                            (long long)seqs[i], t);
+            if ((int64_t)s->tokens + t > INT_MAX)
+                return fail(PA_ERR_INVALID_ARG, "sequence %lld outgrows 32 bits", (long long)seqs[i]);
+            const int64_t after = blocks_for((int64_t)s->tokens + t, bs);
+            if (after > max_blocks_per_seq || (int64_t)s->table.size() > max_blocks_per_seq)
+                return fail(PA_ERR_INVALID_ARG, "sequence %lld outgrows max_blocks_per_seq %d",
+                            (long long)seqs[i], max_blocks_per_seq);
+            s->table.reserve((size_t)after);
+            nodes += t;
+            need += after - blocks_for(s->tokens, bs);
+            if (t > 0 && s->tokens % bs != 0) {
+                const int32_t last = s->table.back();
+                if (bm->ref[last] - drops[last] > 1) {
+                    ++need;
+                    ++drops[last];
+                }
+            }
+        }
+    } catch (...) {
+        return fail(PA_ERR_INVALID_ARG, "out of host memory");
+    }
+    if (nodes > INT_MAX)
+        return fail(PA_ERR_INVALID_ARG, "%lld nodes in one step", (long long)nodes);
+    if (nodes > 0 && !slot_mapping)
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    if ((size_t)need > bm->free_list.size())
+        return fail(PA_ERR_INVALID_ARG, "pool exhausted: the step needs %lld blocks, %zu free",
+                    (long long)need, bm->free_list.size());
+    int32_t pairs = 0, at = 0;
+    tree_start[0] = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        context_lens[i] = bm->find(seqs[i])->tokens;
+        for (int32_t k = 0; k < tree_sizes[i]; ++k) {
+            int64_t src, dst;
+            pa_bm_append_token(bm, seqs[i], &slot_mapping[at++], &src, &dst);
+            if (src >= 0) { // the first node only: the block is exclusive afterwards
+                copy_pairs[2 * pairs] = src;
+                copy_pairs[2 * pairs + 1] = dst;
+                ++pairs;
+            }
+        }
+        tree_start[i + 1] = at;
+        const pa_block_manager::Seq *s = bm->find(seqs[i]);
+        int32_t *row = block_tables + (size_t)i * max_blocks_per_seq;
+        std::copy(s->table.begin(), s->table.end(), row);
+        std::fill(row + s->table.size(), row + max_blocks_per_seq, -1);
+    }
+    if (num_pairs)
+        *num_pairs = pairs;
+    return ok();
+}
+
+pa_status pa_bm_truncate(pa_block_manager *bm, int64_t seq, int32_t tokens)
+{
+    if (!bm)
+        return fail(PA_ERR_INVALID_ARG, "NULL block manager");
+    pa_block_manager::Seq *s = bm->find(seq);
+    if (!s)
+        return fail(PA_ERR_INVALID_ARG, "unknown sequence %lld", (long long)seq);
+    if (tokens < 0 || tokens > s->tokens)
+        return fail(PA_ERR_INVALID_ARG, "sequence %lld: cannot keep %d of %d tokens",
+                    (long long)seq, tokens, s->tokens);
+    const size_t keep = (size_t)blocks_for(tokens, bm->block_size);
+    while (s->table.size() > keep) {
+        bm->release(s->table.back());
+        s->table.pop_back();
+    }
+    s->tokens = tokens;
     return ok();
 }
 

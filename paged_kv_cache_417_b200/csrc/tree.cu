@@ -1,0 +1,254 @@
+// tree.cu - the C ABI's calls for trees of drafted tokens: host-side argument
+// checks and kernel launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "pagedkv.h"
+
+#include "host.h"
+#include "last_error.h"
+#include "tree_decode.cuh"
+#include "tree_ops.cuh"
+
+using namespace pagedkv;
+
+namespace {
+
+constexpr int kMaxTreeGroup = 128; // query heads per K/V head
+
+pa_status check_tree_sizes(int32_t num_seqs, int32_t num_tokens)
+{
+    if (num_seqs < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "negative size argument");
+    if (num_seqs > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+    return PA_OK;
+}
+
+pa_status check_mask_words(int32_t mask_words)
+{
+    if (mask_words < 1 || mask_words > PA_TREE_MAX_NODES / 32)
+        return fail(PA_ERR_INVALID_ARG, "mask_words %d outside [1, %d]", mask_words,
+                    PA_TREE_MAX_NODES / 32);
+    return PA_OK;
+}
+
+template <typename T, typename QT>
+cudaError_t launch_tree_decode(const TreeDecodeParams &p, int head_dim, cudaStream_t st)
+{
+    const dim3 grid(p.num_tokens, (p.num_heads + 3) / 4);
+    return head_dim == 64 ? launch_pdl(tree_decode_kernel<T, QT, 64>, grid, dim3(128), 0, st, p)
+                          : launch_pdl(tree_decode_kernel<T, QT, 128>, grid, dim3(128), 0, st, p);
+}
+
+} // namespace
+
+extern "C" {
+
+pa_status pa_tree_mask(int32_t *mask, int32_t *depth, const int32_t *parents,
+                       const int32_t *tree_start, int32_t num_seqs, int32_t num_tokens,
+                       int32_t mask_words, int32_t *dev_err, void *stream)
+{
+    pa_status s = check_tree_sizes(num_seqs, num_tokens);
+    if (s != PA_OK)
+        return s;
+    if ((s = check_mask_words(mask_words)) != PA_OK)
+        return s;
+    if (num_seqs == 0)
+        return ok();
+    if (!tree_start || (num_tokens > 0 && (!mask || !parents)))
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    static std::atomic<size_t> smem_set[kMaxDevices];
+    const auto smem_for = [](int words) {
+        return (size_t)32 * words * ((words | 1) + 2) * sizeof(int32_t);
+    };
+    cudaError_t e = allow_smem(tree_mask_kernel, smem_for(PA_TREE_MAX_NODES / 32), smem_set);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute(tree_mask)");
+    TreeMaskParams p;
+    p.mask = mask;
+    p.depth = depth;
+    p.parents = parents;
+    p.tree_start = tree_start;
+    p.dev_err = dev_err;
+    p.num_tokens = num_tokens;
+    p.mask_words = mask_words;
+    e = launch_pdl(tree_mask_kernel, dim3(num_seqs), dim3(32 * mask_words), smem_for(mask_words),
+                   static_cast<cudaStream_t>(stream), p);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_mask launch");
+    return ok();
+}
+
+size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache)
+{
+    if (check_cache(cache) != PA_OK)
+        return (size_t)-1;
+    ok();
+    return 16;
+}
+
+pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,
+                         int32_t num_tokens, int32_t num_heads, const void *key_cache,
+                         const void *value_cache, const pa_cache_desc *cache,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, const int32_t *tree_start,
+                         const int32_t *mask, int32_t mask_words, float scale, void *workspace,
+                         size_t workspace_bytes, int32_t *dev_err, void *stream)
+{
+    pa_status s = check_cache(cache);
+    if (s != PA_OK)
+        return s;
+    if ((s = check_tree_sizes(num_seqs, num_tokens)) != PA_OK)
+        return s;
+    if (num_heads <= 0 || max_blocks_per_seq < 0)
+        return fail(PA_ERR_INVALID_ARG, "negative size argument");
+    if (num_heads % cache->num_kv_heads != 0)
+        return fail(PA_ERR_UNSUPPORTED, "num_heads %d is not a multiple of num_kv_heads %d",
+                    num_heads, cache->num_kv_heads);
+    if (num_heads / cache->num_kv_heads > kMaxTreeGroup)
+        return fail(PA_ERR_UNSUPPORTED, "%d query heads per K/V head (at most %d)",
+                    num_heads / cache->num_kv_heads, kMaxTreeGroup);
+    if (out_dtype != PA_F16 && out_dtype != PA_BF16 && out_dtype != PA_F32)
+        return fail(PA_ERR_INVALID_ARG, "out_dtype %d", (int)out_dtype);
+    if ((s = check_mask_words(mask_words)) != PA_OK)
+        return s;
+    if (!(scale == scale))
+        return fail(PA_ERR_INVALID_ARG, "scale is NaN");
+    if (num_seqs == 0 || num_tokens == 0)
+        return ok();
+    if (!out || !query || !key_cache || !value_cache || !context_lens || !tree_start || !mask ||
+        (max_blocks_per_seq > 0 && !block_tables))
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
+        return fail(PA_ERR_INVALID_ARG, "query and caches must be 16-byte aligned");
+    const size_t need = pa_tree_decode_workspace_size(cache);
+    if (!workspace || workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
+    if (!aligned16(workspace))
+        return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    TreeDecodeParams p;
+    p.out = out;
+    p.query = query;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.tree_start = tree_start;
+    p.mask = mask;
+    p.dev_err = dev_err;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_heads = num_heads;
+    p.num_kv_heads = cache->num_kv_heads;
+    p.num_blocks = cache->num_blocks;
+    p.block_size = cache->block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.mask_words = mask_words;
+    p.out_dtype = (int32_t)out_dtype;
+    p.qk_scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (cache->dtype == PA_F16)
+        e = launch_tree_decode<__half, __half>(p, cache->head_dim, st);
+    else if (cache->dtype == PA_BF16)
+        e = launch_tree_decode<__nv_bfloat16, __nv_bfloat16>(p, cache->head_dim, st);
+    else if (cache->io_dtype == PA_F16)
+        e = launch_tree_decode<E4M3, __half>(p, cache->head_dim, st);
+    else
+        e = launch_tree_decode<E4M3, __nv_bfloat16>(p, cache->head_dim, st);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_decode launch");
+    return ok();
+}
+
+pa_status pa_tree_accept(int32_t *accepted, int32_t *accepted_lens, int64_t *next_token,
+                         const int32_t *parents, const int32_t *tree_start,
+                         const int64_t *draft_tokens, const int64_t *target_tokens,
+                         int32_t num_seqs, int32_t num_tokens, int32_t max_path,
+                         int32_t *dev_err, void *stream)
+{
+    pa_status s = check_tree_sizes(num_seqs, num_tokens);
+    if (s != PA_OK)
+        return s;
+    if (max_path < 1 || max_path > PA_TREE_MAX_NODES)
+        return fail(PA_ERR_INVALID_ARG, "max_path %d outside [1, %d]", max_path,
+                    PA_TREE_MAX_NODES);
+    if (num_seqs == 0)
+        return ok();
+    if (!accepted || !accepted_lens || !next_token || !tree_start ||
+        (num_tokens > 0 && (!parents || !draft_tokens || !target_tokens)))
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    TreeAcceptParams p;
+    p.accepted = accepted;
+    p.accepted_lens = accepted_lens;
+    p.next_token = next_token;
+    p.parents = parents;
+    p.tree_start = tree_start;
+    p.draft_tokens = draft_tokens;
+    p.target_tokens = target_tokens;
+    p.dev_err = dev_err;
+    p.num_tokens = num_tokens;
+    p.max_path = max_path;
+    cudaError_t e = launch_pdl(tree_accept_kernel, dim3(num_seqs), dim3(256), 0,
+                               static_cast<cudaStream_t>(stream), p);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_accept launch");
+    return ok();
+}
+
+pa_status pa_tree_compact(void *const *key_caches, void *const *value_caches,
+                          int32_t num_layers, const pa_cache_desc *cache,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq,
+                          const int32_t *context_lens, const int32_t *accepted,
+                          const int32_t *accepted_lens, int32_t num_seqs, int32_t max_path,
+                          int32_t *dev_err, void *stream)
+{
+    pa_status s = check_cache(cache);
+    if (s != PA_OK)
+        return s;
+    if ((s = check_tree_sizes(num_seqs, 0)) != PA_OK)
+        return s;
+    if (num_layers < 1 || num_layers > PA_MAX_LAYERS)
+        return fail(PA_ERR_INVALID_ARG, "num_layers %d outside [1, %d]", num_layers, PA_MAX_LAYERS);
+    if (max_path < 1 || max_path > PA_TREE_MAX_NODES || max_blocks_per_seq < 0)
+        return fail(PA_ERR_INVALID_ARG, "max_path %d (1 .. %d) or max_blocks_per_seq %d", max_path,
+                    PA_TREE_MAX_NODES, max_blocks_per_seq);
+    if (num_seqs == 0)
+        return ok();
+    if (!key_caches || !value_caches || !context_lens || !accepted || !accepted_lens ||
+        (max_blocks_per_seq > 0 && !block_tables))
+        return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
+    CompactParams p;
+    std::memset(&p, 0, sizeof(p));
+    for (int l = 0; l < num_layers; ++l) {
+        if (!key_caches[l] || !value_caches[l])
+            return fail(PA_ERR_INVALID_ARG, "NULL cache pointer for layer %d", l);
+        if (!aligned16(key_caches[l]) || !aligned16(value_caches[l]))
+            return fail(PA_ERR_INVALID_ARG, "cache of layer %d not 16-byte aligned", l);
+        p.key_caches[l] = key_caches[l];
+        p.value_caches[l] = value_caches[l];
+    }
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.accepted = accepted;
+    p.accepted_lens = accepted_lens;
+    p.dev_err = dev_err;
+    p.num_blocks = cache->num_blocks;
+    p.block_size = cache->block_size;
+    p.num_heads = cache->num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_path = max_path;
+    p.scaled = cache->dtype == PA_FP8_E4M3;
+    p.row_vecs = cache->head_dim * (p.scaled ? 1 : 2) / 16;
+    p.tile_bytes = (int32_t)tile_bytes(cache);
+    cudaError_t e = launch_pdl(tree_compact_kernel, dim3(num_seqs, num_layers, 2), dim3(128), 0,
+                               static_cast<cudaStream_t>(stream), p);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_compact launch");
+    return ok();
+}
+
+} // extern "C"
