@@ -347,7 +347,8 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
  * context_lens[s] cached tokens and those nodes j of its own tree whose bit
  * is set in its mask row, all reached through the block table.
  *
- * out         device [num_tokens][num_heads][head_dim] of out_dtype.
+ * out         device [num_tokens][num_heads][head_dim] of out_dtype, 16-byte
+ *             aligned.
  * query       device [num_tokens][num_heads][head_dim], cache dtype (fp8
  *             caches: the descriptor's io_dtype), 16-byte aligned. The group
  *             size num_heads / num_kv_heads is at most 128.

@@ -10,6 +10,7 @@
 #include "host.h"
 #include "last_error.h"
 #include "tree_decode.cuh"
+#include "tree_decode_simple.cuh"
 #include "tree_ops.cuh"
 
 using namespace pagedkv;
@@ -36,11 +37,110 @@ pa_status check_mask_words(int32_t mask_words)
 }
 
 template <typename T, typename QT>
-cudaError_t launch_tree_decode(const TreeDecodeParams &p, int head_dim, cudaStream_t st)
+cudaError_t launch_tree_simple(const TreeSimpleParams &p, int head_dim, cudaStream_t st)
 {
     const dim3 grid(p.num_tokens, (p.num_heads + 3) / 4);
     return head_dim == 64 ? launch_pdl(tree_decode_kernel<T, QT, 64>, grid, dim3(128), 0, st, p)
                           : launch_pdl(tree_decode_kernel<T, QT, 128>, grid, dim3(128), 0, st, p);
+}
+
+int tree_ctas() { return kTreeCtasPerSm * sm_count_of_current_device(); }
+
+// Workspace: [records][partial rows][(m, l) pairs], each 256-byte aligned.
+struct TreeWorkspace {
+    size_t acc, ml, bytes;
+};
+
+TreeWorkspace tree_workspace(int ctas, int head_dim)
+{
+    const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    TreeWorkspace w;
+    w.acc = up((size_t)ctas * sizeof(TreeMergeRecord));
+    w.ml = w.acc + up((size_t)ctas * 2 * kTreeRows * head_dim * sizeof(float));
+    w.bytes = w.ml + up((size_t)ctas * 2 * kTreeRows * sizeof(float2));
+    return w;
+}
+
+// Query rows as (64 elements, heads, nodes, halves of a row): a box holds one
+// half of the group's heads of a tile's nodes, rows of 128 bytes in order.
+pa_status encode_tree_query(CUtensorMap *map, const void *query, int num_tokens, int num_heads,
+                            int group, int head_dim)
+{
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc)
+        return fail(PA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t row = (cuuint64_t)head_dim * 2;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)num_heads, (cuuint64_t)num_tokens,
+                                (cuuint64_t)head_dim / 64};
+    const cuuint64_t strides[3] = {row, row * num_heads, 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)(kTreeRows / group), 1};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(query), dims,
+                           strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return PA_OK;
+}
+
+// A 16-bit pool as (64 elements, 8 rows, halves of a row, groups of 8 rows):
+// a box is one (block, head) tile, in the layout tree_decode.cuh describes.
+pa_status encode_tree_pool(CUtensorMap *map, const void *pool, const pa_cache_desc *c)
+{
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc)
+        return fail(PA_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t row = (cuuint64_t)c->head_dim * 2;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)c->head_dim / 64,
+                                (cuuint64_t)c->num_blocks * c->num_kv_heads * c->block_size / 8};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)c->head_dim / 64, (cuuint32_t)c->block_size / 8};
+    const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(pool), dims,
+                           strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return PA_OK;
+}
+
+template <typename QT, int D, int BS>
+pa_status launch_tree(const TreeTmaParams &g, int ctas, cudaStream_t st)
+{
+    using C = TreeCfg<QT, D, BS>;
+    auto kernel = tree_decode_tc_kernel<QT, D, BS>;
+    static std::atomic<size_t> smem_set[kMaxDevices];
+    cudaError_t e = allow_smem(kernel, C::kSmem, smem_set);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "cudaFuncSetAttribute(tree_decode)");
+    e = launch_pdl(kernel, dim3(ctas), dim3(C::kThreads), C::kSmem, st, g);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_decode launch");
+    e = launch_pdl(tree_merge_kernel<D>, dim3(ctas - 1, D / 16), dim3(kTreeRows), 0, st, g.p);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree_merge launch");
+    return ok();
+}
+
+template <typename QT, int D>
+pa_status launch_tree_bs(const TreeTmaParams &g, int block_size, int ctas, cudaStream_t st)
+{
+    switch (block_size) {
+    case 8: return launch_tree<QT, D, 8>(g, ctas, st);
+    case 16: return launch_tree<QT, D, 16>(g, ctas, st);
+    case 32: return launch_tree<QT, D, 32>(g, ctas, st);
+    }
+    return fail(PA_ERR_UNSUPPORTED, "block_size %d", block_size);
+}
+
+template <typename QT>
+pa_status launch_tree_dim(const TreeTmaParams &g, const pa_cache_desc *c, int ctas,
+                          cudaStream_t st)
+{
+    return c->head_dim == 64 ? launch_tree_bs<QT, 64>(g, c->block_size, ctas, st)
+                             : launch_tree_bs<QT, 128>(g, c->block_size, ctas, st);
 }
 
 } // namespace
@@ -87,7 +187,7 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache)
     if (check_cache(cache) != PA_OK)
         return (size_t)-1;
     ok();
-    return 16;
+    return tree_workspace(tree_ctas(), cache->head_dim).bytes;
 }
 
 pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,
@@ -122,46 +222,78 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     if (!out || !query || !key_cache || !value_cache || !context_lens || !tree_start || !mask ||
         (max_blocks_per_seq > 0 && !block_tables))
         return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
-    if (!aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
-        return fail(PA_ERR_INVALID_ARG, "query and caches must be 16-byte aligned");
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key_cache) || !aligned16(value_cache))
+        return fail(PA_ERR_INVALID_ARG, "out, query and caches must be 16-byte aligned");
+    if (cache->num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty pool");
+    if ((int64_t)cache->num_blocks * cache->num_kv_heads * (cache->block_size / 8) > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "pool of more than 2^34 rows");
     const size_t need = pa_tree_decode_workspace_size(cache);
     if (!workspace || workspace_bytes < need)
         return fail(PA_ERR_WORKSPACE, "workspace of %zu bytes, need %zu", workspace_bytes, need);
     if (!aligned16(workspace))
         return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-    TreeDecodeParams p;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (cache->dtype == PA_FP8_E4M3) {
+        TreeSimpleParams p;
+        p.out = out;
+        p.query = query;
+        p.key_cache = key_cache;
+        p.value_cache = value_cache;
+        p.block_tables = block_tables;
+        p.context_lens = context_lens;
+        p.tree_start = tree_start;
+        p.mask = mask;
+        p.dev_err = dev_err;
+        p.num_seqs = num_seqs;
+        p.num_tokens = num_tokens;
+        p.num_heads = num_heads;
+        p.num_kv_heads = cache->num_kv_heads;
+        p.num_blocks = cache->num_blocks;
+        p.block_size = cache->block_size;
+        p.max_blocks_per_seq = max_blocks_per_seq;
+        p.mask_words = mask_words;
+        p.out_dtype = (int32_t)out_dtype;
+        p.qk_scale_log2 = scale * 1.4426950408889634f;
+        const cudaError_t e = cache->io_dtype == PA_F16
+                                  ? launch_tree_simple<E4M3, __half>(p, cache->head_dim, st)
+                                  : launch_tree_simple<E4M3, __nv_bfloat16>(p, cache->head_dim, st);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "tree_decode launch");
+        return ok();
+    }
+    TreeTmaParams g;
+    std::memset(&g, 0, sizeof(g));
+    TreeDecodeParams &p = g.p;
+    const int ctas = tree_ctas();
+    const TreeWorkspace w = tree_workspace(ctas, cache->head_dim);
+    char *ws = static_cast<char *>(workspace);
     p.out = out;
-    p.query = query;
-    p.key_cache = key_cache;
-    p.value_cache = value_cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.tree_start = tree_start;
     p.mask = mask;
     p.dev_err = dev_err;
+    p.ws_records = reinterpret_cast<TreeMergeRecord *>(ws);
+    p.ws_acc = reinterpret_cast<float4 *>(ws + w.acc);
+    p.ws_ml = reinterpret_cast<float2 *>(ws + w.ml);
     p.num_seqs = num_seqs;
     p.num_tokens = num_tokens;
     p.num_heads = num_heads;
     p.num_kv_heads = cache->num_kv_heads;
+    p.group = num_heads / cache->num_kv_heads;
     p.num_blocks = cache->num_blocks;
-    p.block_size = cache->block_size;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.mask_words = mask_words;
     p.out_dtype = (int32_t)out_dtype;
     p.qk_scale_log2 = scale * 1.4426950408889634f;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (cache->dtype == PA_F16)
-        e = launch_tree_decode<__half, __half>(p, cache->head_dim, st);
-    else if (cache->dtype == PA_BF16)
-        e = launch_tree_decode<__nv_bfloat16, __nv_bfloat16>(p, cache->head_dim, st);
-    else if (cache->io_dtype == PA_F16)
-        e = launch_tree_decode<E4M3, __half>(p, cache->head_dim, st);
-    else
-        e = launch_tree_decode<E4M3, __nv_bfloat16>(p, cache->head_dim, st);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "tree_decode launch");
-    return ok();
+    if ((s = encode_tree_query(&g.q, query, num_tokens, num_heads, p.group, cache->head_dim)) !=
+            PA_OK ||
+        (s = encode_tree_pool(&g.k, key_cache, cache)) != PA_OK ||
+        (s = encode_tree_pool(&g.v, value_cache, cache)) != PA_OK)
+        return s;
+    return cache->dtype == PA_F16 ? launch_tree_dim<__half>(g, cache, ctas, st)
+                                  : launch_tree_dim<__nv_bfloat16>(g, cache, ctas, st);
 }
 
 pa_status pa_tree_accept(int32_t *accepted, int32_t *accepted_lens, int64_t *next_token,

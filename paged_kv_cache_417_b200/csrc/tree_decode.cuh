@@ -4,11 +4,53 @@
 // j running over the cached tokens of node i's sequence and over the nodes of
 // its tree whose mask bit is set.
 //
-// tree_decode_kernel: one warp per (node, query head), a lane holding D/32
-// dims, one token at a time with an online softmax in base 2.
+// Work. The G query heads of a K/V head and kTreeRows / G consecutive nodes
+// make a tile of up to 128 rows that share every key and value: a unit is
+// (sequence, K/V head, row tile), its keys cut into tiles of 64 tokens. All
+// tiles of all units stand in one line (sequence, head, row tile, tokens
+// innermost) that the grid's CTAs, two per SM, cut into equal pieces, whatever
+// the lengths: each CTA adds up the lengths itself, so nothing about them is
+// needed on the host. A unit cut by the end of a piece leaves partial results
+// (m, l, unnormalised rows) in the workspace, at most two per CTA, and
+// tree_merge_kernel joins them with the log-sum-exp rule. Row tiles of one
+// head follow one another, so their keys come from L2 after the first.
+//
+// Roles of a CTA's warps:
+//   0-3  one thread per row: softmax, and the rescaling and writing of rows
+//   4    fetches Q, K and V by TMA, block by block through the block table
+//   5    issues the MMAs: S = Q K^T (128 x 64, both operands in shared
+//        memory) and O += P V (128 x D, P in tensor memory)
+// Tensor memory (256 columns a CTA): O in D fp32 columns and two S tiles of
+// 64; P, 16 bits, overwrites the S tile it comes from. S of the next tile is
+// multiplied before P V of this one, so the tensor core works while the
+// softmax runs; the other CTA of the SM fills what is left.
+//
+// Softmax, base 2: p = 2^(s*c - m + kTreeBias), c = scale * log2(e). m is a
+// row's reference, not its maximum: it moves (and O and l are rescaled) only
+// when a score exceeds it by more than kTreeSlack, which after the first
+// tiles of a context is rare. p is then at most 2^(kTreeBias + kTreeSlack),
+// inside f16's range, and an f16 p keeps its full precision down to 2^-22 of
+// the reference.
+//
+// Masks. A tile that ends before the context does is seen by every row. Tiles
+// at and behind the context's end take the slower path: scores that a row
+// does not see are replaced before the maximum and their weights by zero. A
+// product 0 * NaN would still reach a row, so V rows behind the last token
+// are zeroed in shared memory, and a tree node's V row that holds a NaN or an
+// infinity is taken out of the tile and added to the rows that see it one by
+// one (rescue_rows).
+//
+// Layouts. K and V blocks lie in shared memory as [8-row group][64-element
+// half][8 rows][128 bytes], swizzled, which one 4-D box per block fetches
+// whatever the block size. As an operand that is K-major for Q K^T (a row
+// group every D / 64 KiB) and MN-major for P V.
 #pragma once
 
+#include <climits>
 #include <cstdint>
+#include <type_traits>
+
+#include <cuda.h>
 
 #include "decode.cuh"
 #include "pagedkv.h"
@@ -17,124 +59,921 @@
 
 namespace pagedkv {
 
+constexpr int kTreeRows = 128;  // rows of a tile: the MMA's M
+constexpr int kTreeTile = 64;   // tokens of a tile
+constexpr int kTreeCtasPerSm = 2;
+constexpr float kTreeSlack = 6.f;
+constexpr float kTreeBias = 8.f;
+
+// Where a unit cut between CTAs b-1 and b (and not before) has its parts:
+// part 0 in CTA b-1's second slot, parts 1 .. parts-1 in the first slots of
+// CTAs b .. b+parts-2.
+struct TreeMergeRecord {
+    int32_t parts; // 0: no unit to merge here
+    int32_t rows;
+    int32_t first_row; // row of out of the tile's first node
+    int32_t kv_head;
+};
+
 struct TreeDecodeParams {
     void *out;
-    const void *query, *key_cache, *value_cache;
     const int32_t *block_tables, *context_lens, *tree_start, *mask;
     int32_t *dev_err;
-    int32_t num_seqs, num_tokens, num_heads, num_kv_heads, num_blocks, block_size;
+    TreeMergeRecord *ws_records; // [CTAs]
+    float4 *ws_acc;              // [CTAs][2][D / 4][kTreeRows]
+    float2 *ws_ml;               // [CTAs][2][kTreeRows] = (m, l)
+    int32_t num_seqs, num_tokens, num_heads, num_kv_heads, group, num_blocks;
     int32_t max_blocks_per_seq, mask_words, out_dtype;
     float qk_scale_log2;
 };
 
-// The first sequence that row r belongs to, -1 for padding: the lanes of a
-// warp look through the offsets.
-__device__ __forceinline__ int sequence_of_row(const TreeDecodeParams &p, int limit, int r,
-                                               int lane)
+struct TreeTmaParams {
+    CUtensorMap q, k, v;
+    TreeDecodeParams p;
+};
+
+// A sequence's share of the line of tiles.
+struct TreeSeq {
+    int32_t first, nodes;  // rows of the packed arrays; nodes 0: nothing to do
+    int32_t ctx;
+    int32_t row_tiles, tiles; // tiles: of one unit
+    int32_t error;            // PA_DEVERR_* bits
+    bool bad_context;         // rows become NaN (one tile per unit, nothing read)
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeDecodeParams &p, int s, int bs)
 {
-    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-        bool mine = false;
-        if (s0 + lane < p.num_seqs) {
-            const TreeSpan t = tree_span(p.tree_start, s0 + lane, p.num_tokens, limit);
-            mine = t.size > 0 && t.first <= r && r - t.first < t.size;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, mine);
-        if (hit)
-            return s0 + __ffs(hit) - 1;
-    }
-    return -1;
+    TreeSeq q;
+    const TreeSpan t =
+        tree_span(p.tree_start, s, p.num_tokens, min(32 * p.mask_words, PA_TREE_MAX_NODES));
+    q.first = t.first;
+    q.nodes = max(t.size, 0);
+    q.error = t.size < 0 ? PA_DEVERR_TREE : 0;
+    q.ctx = p.context_lens[s];
+    // Below 2^31 by two tiles, so that no sum of positions overflows.
+    const int64_t capacity =
+        min((int64_t)p.max_blocks_per_seq * bs, (int64_t)INT_MAX - 2 * kTreeTile);
+    q.bad_context = q.nodes > 0 && (q.ctx < 0 || (int64_t)q.ctx + q.nodes > capacity);
+    if (q.bad_context)
+        q.error |= PA_DEVERR_CONTEXT_LEN;
+    const int per_tile = kTreeRows / p.group;
+    q.row_tiles = (q.nodes + per_tile - 1) / per_tile;
+    q.tiles = q.nodes == 0       ? 0
+              : q.bad_context ? 1
+                              : (int)(((int64_t)q.ctx + q.nodes + kTreeTile - 1) / kTreeTile);
+    return q;
 }
 
-template <typename T, int D> struct TreeRow; // D/32 elements of a cached row per lane
-template <int D> struct TreeRow<E4M3, D> {
-    static __device__ __forceinline__ void load(const void *cache, int64_t tile, int off, int bs,
-                                                int lane, float (&x)[D / 32])
+__device__ __forceinline__ int64_t tree_seq_tiles(const TreeDecodeParams &p, const TreeSeq &q)
+{
+    return (int64_t)q.tiles * q.row_tiles * p.num_kv_heads;
+}
+
+// What a CTA does: its tiles, and where they begin. Of n = `ctas` pieces of
+// the line, piece b begins at b * total / n.
+struct TreePlan {
+    int64_t begin, end;   // of the line
+    int64_t seq_begin;    // first tile of sequence `seq`
+    int64_t each;         // total / ctas
+    int32_t seq, ctas, rest; // rest: total % ctas
+
+    __device__ __forceinline__ int64_t piece(int b) const
     {
-        const uint8_t *t = static_cast<const uint8_t *>(cache) + tile * (bs * D + 4 * bs);
-        const float scale = *reinterpret_cast<const float *>(t + bs * D + 4 * off);
-        for (int e = 0; e < D / 32; ++e)
-            x[e] = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3 *>(
-                       t)[off * D + lane * (D / 32) + e]) * scale;
-    }
-};
-template <typename T, int D> struct TreeRow {
-    static __device__ __forceinline__ void load(const void *cache, int64_t tile, int off, int bs,
-                                                int lane, float (&x)[D / 32])
-    {
-        const T *t = static_cast<const T *>(cache) + (tile * bs + off) * D + lane * (D / 32);
-        for (int e = 0; e < D / 32; ++e)
-            x[e] = static_cast<float>(t[e]);
+        return b * each + (uint32_t)(b * rest) / (uint32_t)ctas;
     }
 };
 
-template <typename T, typename QT, int D>
-__global__ void __launch_bounds__(128) tree_decode_kernel(
+// Adds up the tiles of all sequences, every thread of the CTA taking part;
+// `plan` and `sums` (32 entries) are in shared memory. Ends with a barrier.
+__device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, TreePlan *plan,
+                                          int64_t *sums)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nwarps = blockDim.x >> 5;
+    const bool one = p.num_seqs <= (int)blockDim.x; // the usual case: one sequence per thread
+    int64_t total = 0, mine = 0, before = 0;
+    int32_t error = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
+        const int s = s0 + tid;
+        if (s < p.num_seqs) {
+            const TreeSeq q = tree_seq(p, s, bs);
+            error |= q.error;
+            mine = tree_seq_tiles(p, q);
+            total += mine;
+        }
+    }
+    if (error && blockIdx.x == 0)
+        report(p.dev_err, error);
+    int64_t upto = one ? mine : total; // inclusive sums over threads
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o)
+            upto += x;
+    }
+    if (lane == 31)
+        sums[warp] = upto;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < nwarps; ++w) {
+        if (w == warp)
+            before = total;
+        total += sums[w];
+    }
+    const int ctas = (int)min((int64_t)gridDim.x, total);
+    if (tid == 0) {
+        plan->ctas = ctas;
+        plan->begin = plan->end = 0;
+        if ((int)blockIdx.x < ctas) {
+            plan->each = total / ctas;
+            plan->rest = (int)(total % ctas);
+            plan->begin = plan->piece(blockIdx.x);
+            plan->end = plan->piece(blockIdx.x + 1);
+        }
+    }
+    __syncthreads();
+    if ((int)blockIdx.x >= ctas)
+        return;
+    const int64_t begin = plan->begin;
+    if (one) {
+        const int64_t first = before + upto - mine;
+        if (mine > 0 && first <= begin && begin < first + mine) {
+            plan->seq = tid;
+            plan->seq_begin = first;
+        }
+        __syncthreads();
+        return;
+    }
+    // More sequences than threads: again, in order, until the piece is found.
+    int64_t base = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
+        mine = 0;
+        if (s0 + tid < p.num_seqs)
+            mine = tree_seq_tiles(p, tree_seq(p, s0 + tid, bs));
+        upto = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o)
+                upto += x;
+        }
+        __syncthreads();
+        if (lane == 31)
+            sums[warp] = upto;
+        __syncthreads();
+        int64_t chunk = 0;
+        for (int w = 0; w < nwarps; ++w) {
+            if (w == warp)
+                before = chunk;
+            chunk += sums[w];
+        }
+        const int64_t first = base + before + upto - mine;
+        if (mine > 0 && first <= begin && begin < first + mine) {
+            plan->seq = s0 + tid;
+            plan->seq_begin = first;
+        }
+        base += chunk;
+        if (base > begin)
+            break; // the same for every thread
+    }
+    __syncthreads();
+}
+
+// One unit's share of a CTA's piece, as the fetching warp hands it on.
+struct TreeSegment {
+    int32_t tile0, tile1; // tokens [64 * tile0, 64 * tile1)
+    int32_t ctx, n;       // cached tokens, and with the tree
+    int32_t row0;         // packed row of the tile's first node
+    int32_t rows;         // live rows of the tile
+    int32_t kv_head;
+    int32_t slot;         // -1: writes its rows; 0, 1: leaves a part in that slot
+    int32_t last;         // 1: the CTA's last segment
+};
+
+template <typename T, int D, int BS> struct TreeCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTileBytes = kTreeTile * D * 2;       // a K or V tile
+    static constexpr int kQBytes = kTreeRows * D * 2;
+    static constexpr int kGroupBytes = 1024 * kHalves;         // 8 rows
+    static constexpr int kStages = D == 128 ? 2 : 4;           // of K and of V
+    static constexpr int kBlocks = kTreeTile / BS;             // blocks of a tile
+    static constexpr int kBlockBytes = BS * D * 2;
+    static constexpr int kThreads = 192;
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
+    static constexpr uint32_t kColumns = 256;
+    static constexpr uint32_t kS0 = D; // tensor-memory column of the first S tile
+};
+
+// Barriers and small state of a CTA.
+template <int NS> struct TreeShared {
+    uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+    // q_full twice: the fetching warp may be two segments ahead of the softmax.
+    uint64_t q_full[2], q_empty, s_full[2], p_full[2], o_full, o_free, warps, drain;
+    TreePlan plan;
+    int64_t sums[32];
+    TreeSegment seg[4];
+    int32_t poison[4];       // segment met a block id outside the pool
+    uint32_t strange[2];     // tokens of a tile whose V row holds NaN or infinity
+    uint32_t tmem;
+    int32_t keep_o;          // tile whose P V adds to O although it is a segment's first
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats to a packed pair, the first in the low half.
+template <typename QT> __device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    uint32_t r;
+    if constexpr (std::is_same<QT, __half>::value)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// Byte address inside a K or V tile of 16-byte piece c (of D / 8) of row j.
+template <int D> __device__ __forceinline__ uint32_t tree_piece_at(int j, int c)
+{
+    return (j >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (j & 7) * 128 +
+           (((c & 7) ^ (j & 7)) << 4);
+}
+
+// Which of the 64 tokens from `t0` on a row sees: those before the context's
+// end, then those whose bit is set in its mask row.
+__device__ __forceinline__ uint64_t tree_seen(const int32_t *words, int num_words, int t0, int ctx,
+                                              int n)
+{
+    const int b0 = t0 - ctx; // node of column 0; negative: cached tokens first
+    uint64_t bits;
+    const auto word = [&](int w) -> uint32_t {
+        return w < num_words ? (uint32_t)words[w] : 0u;
+    };
+    if (b0 >= 0) {
+        const int w = b0 >> 5, sh = b0 & 31;
+        const uint32_t a = word(w), b = word(w + 1), c = sh ? word(w + 2) : 0u;
+        bits = (uint64_t)__funnelshift_r(a, b, sh) | ((uint64_t)__funnelshift_r(b, c, sh) << 32);
+    } else if (b0 > -kTreeTile) {
+        bits = (((uint64_t)word(1) << 32 | word(0)) << -b0) | ((1ull << -b0) - 1);
+    } else {
+        bits = ~0ull;
+    }
+    if (n - t0 < kTreeTile)
+        bits &= n > t0 ? (1ull << (n - t0)) - 1 : 0ull;
+    return bits;
+}
+
+// 32 (4) consecutive floats of a row to `out`, rounded to its type.
+__device__ __forceinline__ void store_row32(void *out, int dtype, size_t at, const uint32_t (&o)[32])
+{
+    if (dtype == 2) {
+        uint4 *to = reinterpret_cast<uint4 *>(static_cast<float *>(out) + at);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        return;
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const float a = __uint_as_float(o[2 * k]), b = __uint_as_float(o[2 * k + 1]);
+        w[k] = dtype == 0 ? pack2<__half>(a, b) : pack2<__nv_bfloat16>(a, b);
+    }
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        to[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
+
+__device__ __forceinline__ void store_row4(void *out, int dtype, size_t at, float4 v)
+{
+    if (dtype == 2) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = v;
+        return;
+    }
+    uint2 w;
+    w.x = dtype == 0 ? pack2<__half>(v.x, v.y) : pack2<__nv_bfloat16>(v.x, v.y);
+    w.y = dtype == 0 ? pack2<__half>(v.z, v.w) : pack2<__nv_bfloat16>(v.z, v.w);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = w;
+}
+
+// O += p * v for the `strange` tokens of a V tile, each for the rows that see
+// it; every softmax thread with its own row. `p_column` is the first column
+// of this tile's P in the warp's lanes, `o_column` of O.
+template <typename QT, int D>
+__device__ __noinline__ void rescue_rows(uint64_t strange, uint64_t seen, uint32_t v_tile,
+                                         uint32_t p_column, uint32_t o_column)
+{
+    for (; strange; strange &= strange - 1) {
+        const int j = __ffsll((long long)strange) - 1;
+        const uint32_t pair = tmem_ld_x1(p_column + (j >> 1));
+        const float2 both = Elem<QT>::pair(pair);
+        const float pj = j & 1 ? both.y : both.x;
+        const bool mine = (seen >> j) & 1;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(o_column + c0, o);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint4 raw;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(raw.x), "=r"(raw.y), "=r"(raw.z), "=r"(raw.w)
+                             : "r"(v_tile + tree_piece_at<D>(j, c0 / 8 + c)));
+                float v[8];
+                unpack8_to<QT>(raw, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (mine)
+                        o[8 * c + e] = __float_as_uint(
+                            fmaf(pj, v[e], __uint_as_float(o[8 * c + e])));
+            }
+            tmem_st_x32(o_column + c0, o);
+        }
+        tmem_wait_st();
+    }
+}
+
+// Whether a 16-byte piece of 16-bit elements holds a NaN or an infinity.
+template <typename QT> __device__ __forceinline__ bool not_finite(const uint4 &x)
+{
+    constexpr uint32_t E = std::is_same<QT, __half>::value ? 0x7c00u : 0x7f80u;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        bad |= (w[k] & E) == E || ((w[k] >> 16) & E) == E;
+    return bad;
+}
+
+template <typename QT, int D, int BS>
+__global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
+    tree_decode_tc_kernel(const __grid_constant__ TreeTmaParams g)
+{
+    using C = TreeCfg<QT, D, BS>;
+    constexpr int NS = C::kStages;
+    constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
+    extern __shared__ __align__(1024) uint8_t tree_dyn[];
+    __shared__ TreeShared<NS> sh;
+    const TreeDecodeParams &p = g.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = (smem_addr(tree_dyn) + 1023u) & ~1023u;
+    const uint32_t q_tile = base, k_tiles = base + C::kQBytes,
+                   v_tiles = k_tiles + NS * C::kTileBytes;
+
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_addr(&sh.k_full[i]), 1);
+            mbar_init(smem_addr(&sh.k_empty[i]), 1);
+            mbar_init(smem_addr(&sh.v_full[i]), 1);
+            mbar_init(smem_addr(&sh.v_empty[i]), 1);
+        }
+        mbar_init(smem_addr(&sh.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.q_full[i]), 1);
+            mbar_init(smem_addr(&sh.s_full[i]), 1);
+            mbar_init(smem_addr(&sh.p_full[i]), 4); // one per softmax warp
+        }
+        mbar_init(smem_addr(&sh.o_full), 1);
+        mbar_init(smem_addr(&sh.o_free), 4);
+        mbar_init(smem_addr(&sh.warps), 4);
+        mbar_init(smem_addr(&sh.drain), 1);
+        fence_mbar_init();
+        sh.keep_o = -1;
+        sh.strange[0] = sh.strange[1] = 0;
+    }
+    if (warp == 5)
+        tmem_alloc(smem_addr(&sh.tmem), C::kColumns);
+    tcgen05_fence_before();
+    pdl_wait_prior_grid();
+    tree_plan(p, BS, &sh.plan, sh.sums);
+    tcgen05_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int count = (int)min(sh.plan.end - sh.plan.begin, (int64_t)INT_MAX); // tiles of the CTA
+    bool ok = true;
+    const auto wait = [&](uint64_t &bar, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(smem_addr(&bar), parity, kWaitLimitNs);
+        return ok;
+    };
+
+    if (count == 0) {
+        if (tid == 0)
+            p.ws_records[blockIdx.x].parts = 0;
+    } else if (warp == 4) {
+        // --- fetch: segments, and the tiles of each ----------------------------------------
+        int s = sh.plan.seq;
+        TreeSeq q = tree_seq(p, s, BS);
+        int64_t into = sh.plan.begin - sh.plan.seq_begin; // tile of the sequence
+        int unit = (int)(into / q.tiles), tile = (int)(into - (int64_t)unit * q.tiles);
+        const int per_tile = kTreeRows / p.group;
+        int it = 0, segs = 0;
+        for (int seg = 0; it < count && ok; ++seg) {
+            segs = seg;
+            const int rt = unit % q.row_tiles, h = unit / q.row_tiles;
+            const int end = min(q.tiles, tile + count - it);
+            const int n = q.bad_context ? 0 : q.ctx + q.nodes;
+            const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+            const auto block_id = [&](int t) { // lane's block of tile t, -1: none
+                const int b = t * C::kBlocks + lane;
+                return lane < C::kBlocks && b * BS < n ? table[b] : -1;
+            };
+            int id = block_id(tile);
+            for (const int tile0 = tile; tile < end && ok; ++tile, ++it) {
+                const int st = it % NS;
+                const uint32_t ph = (it / NS) & 1;
+                const int left = n - tile * kTreeTile; // tokens from here on
+                const int blocks = left <= 0 ? 0 : min(C::kBlocks, (left + BS - 1) / BS);
+                const int next = tile + 1 < end ? block_id(tile + 1) : -1;
+                const bool here = lane < blocks;
+                const bool bad = here && (id < 0 || id >= p.num_blocks);
+                const bool any_bad = __any_sync(0xffffffffu, bad);
+                const int64_t row8 =
+                    (((int64_t)(bad ? 0 : id) * p.num_kv_heads + h) * BS) >> 3;
+                if (it >= NS)
+                    wait(sh.k_empty[st], ph ^ 1);
+                if (lane == 0 && ok) {
+                    if (tile == tile0) {
+                        sh.poison[seg & 3] = q.bad_context;
+                    }
+                    if (any_bad) {
+                        report(p.dev_err, PA_DEVERR_BLOCK_ID);
+                        sh.poison[seg & 3] = 1;
+                    }
+                    mbar_arrive_expect_tx(smem_addr(&sh.k_full[st]), blocks * C::kBlockBytes);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (here)
+                    tma_load_4d(k_tiles + st * C::kTileBytes + lane * C::kBlockBytes, &g.k, 0, 0,
+                                0, (int)row8, smem_addr(&sh.k_full[st]));
+                if (tile == tile0) {
+                    if (seg > 0)
+                        wait(sh.q_empty, (seg - 1) & 1);
+                    if (lane == 0 && ok) {
+                        TreeSegment d;
+                        d.tile0 = tile0;
+                        d.tile1 = end;
+                        d.ctx = q.bad_context ? 0 : q.ctx;
+                        d.n = n;
+                        d.row0 = q.first + rt * per_tile;
+                        d.rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
+                        d.kv_head = h;
+                        d.slot = tile0 > 0 ? 0 : end < q.tiles ? 1 : -1;
+                        d.last = it + end - tile0 >= count;
+                        sh.seg[seg & 3] = d;
+                        const int bytes = per_tile * p.group * 128;
+                        mbar_arrive_expect_tx(smem_addr(&sh.q_full[seg & 1]), bytes * C::kHalves);
+                        for (int u = 0; u < C::kHalves; ++u)
+                            tma_load_4d(q_tile + u * (kTreeRows * 128), &g.q, 0, h * p.group,
+                                        d.row0, u, smem_addr(&sh.q_full[seg & 1]));
+                    }
+                }
+                if (it >= NS)
+                    wait(sh.v_empty[st], ph ^ 1);
+                if (lane == 0 && ok)
+                    mbar_arrive_expect_tx(smem_addr(&sh.v_full[st]), blocks * C::kBlockBytes);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                if (here)
+                    tma_load_4d(v_tiles + st * C::kTileBytes + lane * C::kBlockBytes, &g.v, 0, 0,
+                                0, (int)row8, smem_addr(&sh.v_full[st]));
+                id = next;
+            }
+            // The next unit: of this sequence, or of the next one with any.
+            tile = 0;
+            if (++unit == q.row_tiles * p.num_kv_heads && it < count) {
+                unit = 0;
+                for (++s; s < p.num_seqs; s += 32) {
+                    const bool has = s + lane < p.num_seqs && tree_seq(p, s + lane, BS).nodes > 0;
+                    const unsigned hit = __ballot_sync(0xffffffffu, has);
+                    if (hit) {
+                        s += __ffs(hit) - 1;
+                        break;
+                    }
+                }
+                q = tree_seq(p, s, BS);
+            }
+        }
+        if (!ok) { // let the copies in flight land before the CTA goes
+            constexpr uint64_t kDrainNs = 10000000;
+            for (int i = max(0, it - NS + 1); i <= it; ++i) {
+                mbar_wait_bounded(smem_addr(&sh.k_full[i % NS]), (i / NS) & 1, kDrainNs);
+                mbar_wait_bounded(smem_addr(&sh.v_full[i % NS]), (i / NS) & 1, kDrainNs);
+            }
+            mbar_wait_bounded(smem_addr(&sh.q_full[segs & 1]), (segs >> 1) & 1, kDrainNs);
+        }
+    } else if (warp == 5) {
+        // --- MMAs, one thread ---------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kIdescQk = umma_idesc(kBf16, false, kTreeRows, kTreeTile);
+            constexpr uint32_t kIdescPv = umma_idesc(kBf16, true, kTreeRows, D);
+            int it = 0, pending = -1; // tile whose P V is still to be issued
+            bool pending_first = false;
+            int seg = -1, seg_end = 0, segments_read = 0;
+            const auto issue_pv = [&]() {
+                const int st = pending % NS;
+                wait(sh.p_full[pending & 1], (pending >> 1) & 1);
+                wait(sh.v_full[st], (pending / NS) & 1);
+                bool add = !pending_first;
+                if (pending_first) {
+                    if (segments_read > 0)
+                        wait(sh.o_free, (segments_read - 1) & 1);
+                    ++segments_read;
+                    add = *(volatile int32_t *)&sh.keep_o == pending;
+                }
+                if (!ok)
+                    return;
+                tcgen05_fence_after();
+                const uint32_t v = v_tiles + st * C::kTileBytes;
+                const uint32_t a = tmem + C::kS0 + (pending & 1) * kTreeTile;
+#pragma unroll
+                for (int k = 0; k < kTreeTile / 16; ++k)
+                    tcgen05_mma_ts(tmem, a + k * 8,
+                                   umma_desc(v + k * 2 * C::kGroupBytes, 1024, C::kGroupBytes),
+                                   kIdescPv, add || k > 0);
+                tcgen05_commit(smem_addr(&sh.v_empty[st]));
+                tcgen05_commit(smem_addr(&sh.o_full));
+                pending = -1;
+            };
+            for (; it < count && ok; ++it) {
+                const bool first = it == seg_end;
+                if (first) {
+                    if (pending >= 0)
+                        issue_pv();
+                    ++seg;
+                    if (!wait(sh.q_full[seg & 1], (seg >> 1) & 1))
+                        break;
+                    seg_end = it + sh.seg[seg & 3].tile1 - sh.seg[seg & 3].tile0;
+                }
+                const int st = it % NS;
+                if (!wait(sh.k_full[st], (it / NS) & 1))
+                    break;
+                tcgen05_fence_after();
+                const uint32_t k0 = k_tiles + st * C::kTileBytes;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tcgen05_mma_ss(tmem + C::kS0 + (it & 1) * kTreeTile,
+                                   umma_desc(q_tile + (k / 4) * (kTreeRows * 128) + (k % 4) * 32,
+                                             16, 1024),
+                                   umma_desc(k0 + (k / 4) * 1024 + (k % 4) * 32, 16,
+                                             C::kGroupBytes),
+                                   kIdescQk, k > 0);
+                tcgen05_commit(smem_addr(&sh.s_full[it & 1]));
+                tcgen05_commit(smem_addr(&sh.k_empty[st]));
+                if (it + 1 == seg_end)
+                    tcgen05_commit(smem_addr(&sh.q_empty));
+                if (pending >= 0)
+                    issue_pv();
+                pending = it;
+                pending_first = first;
+            }
+            if (ok && pending >= 0)
+                issue_pv();
+            if (!ok) { // MMAs in flight read shared memory and write tensor memory
+                tcgen05_commit(smem_addr(&sh.drain));
+                mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitLimitNs);
+            }
+        }
+    } else {
+        // --- softmax, one thread per row ----------------------------------------------------
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t o_column = tmem + lanes;
+        const float c = p.qk_scale_log2;
+        // Every lane or none: what follows a wait is done by whole warps.
+        const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, wait(bar, parity));
+            return ok;
+        };
+        uint32_t syncs = 0; // of the softmax warps among themselves, bounded like all others
+        const auto sync_warps = [&]() {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sh.warps));
+            return wait_warp(sh.warps, syncs++ & 1);
+        };
+        if (tid == 0) {
+            // The unit that this piece begins inside of, if it was cut here first.
+            const TreePlan &plan = sh.plan;
+            const TreeSeq q = tree_seq(p, plan.seq, BS);
+            const int64_t into = plan.begin - plan.seq_begin;
+            const int unit = (int)(into / q.tiles), tile = (int)(into - (int64_t)unit * q.tiles);
+            const int64_t unit_begin = plan.begin - tile, unit_last = unit_begin + q.tiles - 1;
+            TreeMergeRecord rec = {0, 0, 0, 0};
+            if (tile > 0 && unit_begin >= plan.piece(blockIdx.x - 1)) {
+                int e = blockIdx.x, hi = plan.ctas - 1; // the CTA with the unit's last tile
+                while (e < hi) {
+                    const int mid = (e + hi + 1) / 2;
+                    if (plan.piece(mid) <= unit_last)
+                        e = mid;
+                    else
+                        hi = mid - 1;
+                }
+                const int per_tile = kTreeRows / p.group, rt = unit % q.row_tiles;
+                rec.parts = e - (int)blockIdx.x + 2;
+                rec.rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
+                rec.first_row = q.first + rt * per_tile;
+                rec.kv_head = unit / q.row_tiles;
+            }
+            p.ws_records[blockIdx.x] = rec;
+        }
+        __syncwarp();
+        int it = 0;
+        bool more = true;
+        for (int seg = 0; more && ok; ++seg) {
+            if (!wait_warp(sh.q_full[seg & 1], (seg >> 1) & 1))
+                break;
+            const TreeSegment d = sh.seg[seg & 3];
+            more = !d.last;
+            const int node = tid / p.group; // of the tile
+            const bool live = tid < d.rows;
+            const bool warp_live = warp * 32 < d.rows;
+            const int32_t *words =
+                p.mask + (size_t)(d.row0 + (live ? node : 0)) * p.mask_words;
+            float m = -INFINITY, l = 0.f;
+            bool saw = false, poison = false;
+            for (int tile = d.tile0; tile < d.tile1 && ok; ++tile, ++it) {
+                const uint32_t s_column = tmem + lanes + C::kS0 + (it & 1) * kTreeTile;
+                const int t0 = tile * kTreeTile, st = it % NS;
+                const bool special = t0 + kTreeTile > d.ctx; // uniform over the CTA
+                uint64_t seen = ~0ull;
+                if (special)
+                    seen = live ? tree_seen(words, p.mask_words, t0, d.ctx, d.n) : 0ull;
+                if (!wait_warp(sh.s_full[it & 1], (it >> 1) & 1))
+                    break;
+                tcgen05_fence_after();
+                uint64_t strange = 0;
+                if (special || tile + 1 == d.tile1) {
+                    // V has to be here for what follows, and the fetching
+                    // warp's word on its block ids with it.
+                    if (!wait_warp(sh.v_full[st], (it / NS) & 1))
+                        break;
+                    poison = *(volatile int32_t *)&sh.poison[seg & 3] != 0;
+                }
+                if (special) {
+                    // Two threads a row of V: rows behind the last token
+                    // become zero, rows of nodes are looked through.
+                    const int j = tid >> 1;
+                    const uint32_t v = v_tiles + st * C::kTileBytes;
+                    constexpr int kPieces = D / 16;
+                    bool bad = false;
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i) {
+                        const uint32_t at =
+                            v + tree_piece_at<D>(j, (tid & 1) * kPieces + i);
+                        if (t0 + j >= d.n) {
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at),
+                                         "r"(0)
+                                         : "memory");
+                        } else if (t0 + j >= d.ctx) {
+                            uint4 x;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                         : "r"(at)
+                                         : "memory");
+                            bad |= not_finite<QT>(x);
+                        }
+                    }
+                    if (bad)
+                        atomicOr(&sh.strange[j >> 5], 1u << (j & 31));
+                    fence_proxy_async_smem();
+                    if (!sync_warps())
+                        break;
+                    strange = (uint64_t)*(volatile uint32_t *)&sh.strange[1] << 32 |
+                              *(volatile uint32_t *)&sh.strange[0];
+                }
+                uint32_t x[64];
+                float alpha = 1.f;
+                bool rescale = false;
+                if (warp_live) {
+                    tmem_ld_x64(s_column, x);
+                    float mx[4];
+                    const bool up = c >= 0.f;
+                    if (special) {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if (!((seen >> k) & 1))
+                                x[k] = __float_as_uint(up ? -INFINITY : INFINITY);
+                        saw |= seen != 0;
+                    } else {
+                        saw = true;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = __uint_as_float(x[k]);
+                    if (up) {
+#pragma unroll
+                        for (int k = 4; k < 64; ++k)
+                            mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
+                        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    } else {
+#pragma unroll
+                        for (int k = 4; k < 64; ++k)
+                            mx[k & 3] = fminf(mx[k & 3], __uint_as_float(x[k]));
+                        mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
+                    }
+                    const float top = seen ? mx[0] * c : -INFINITY;
+                    if (top > m + kTreeSlack || (m == -INFINITY && top > m)) {
+                        alpha = m == -INFINITY ? 0.f : ex2(m - top);
+                        rescale = tile > d.tile0;
+                        m = top;
+                    }
+                    const float off = kTreeBias - (m == -INFINITY ? 0.f : m);
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        float w = ex2(fmaf(__uint_as_float(x[k]), c, off));
+                        if (special && !((seen >> k) & 1))
+                            w = 0.f;
+                        sum[k & 3] += w;
+                        x[k] = __float_as_uint(w);
+                    }
+                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        x[k] = pack2<QT>(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                }
+                // O is complete up to the tile before.
+                if (tile > d.tile0) {
+                    if (!wait_warp(sh.o_full, (it - 1) & 1))
+                        break;
+                    tcgen05_fence_after();
+                }
+                if (warp_live) {
+                    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld_x32(o_column + c0, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st_x32(o_column + c0, o);
+                        }
+                    }
+                    tmem_st_x32(s_column, x);
+                    tmem_wait_st();
+                }
+                if (strange) {
+                    const uint32_t v = v_tiles + st * C::kTileBytes;
+                    if (tile == d.tile0) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = 0;
+                        for (int c0 = 0; c0 < D; c0 += 32)
+                            tmem_st_x32(o_column + c0, o);
+                        tmem_wait_st();
+                        if (tid == 0)
+                            *(volatile int32_t *)&sh.keep_o = it;
+                    }
+                    if (warp_live)
+                        rescue_rows<QT, D>(strange, seen, v, s_column, o_column);
+                    if (!sync_warps())
+                        break;
+                    const int j = tid >> 1;
+                    if ((strange >> j) & 1)
+                        for (int i = 0; i < D / 16; ++i)
+                            asm volatile(
+                                "st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                    v + tree_piece_at<D>(j, (tid & 1) * (D / 16) + i)),
+                                "r"(0)
+                                : "memory");
+                    if (tid < 2)
+                        *(volatile uint32_t *)&sh.strange[tid] = 0;
+                    fence_proxy_async_smem();
+                    if (!sync_warps())
+                        break;
+                }
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sh.p_full[it & 1]));
+            }
+            if (!ok || !wait_warp(sh.o_full, (it - 1) & 1))
+                break;
+            tcgen05_fence_after();
+            if (warp_live) {
+                // A row that saw nothing is zero; one that saw only scores of
+                // minus infinity is NaN, as 0/0 is.
+                const bool none = l == 0.f && !saw;
+                if (d.slot < 0) {
+                    const float inv = none ? 0.f : 1.f / l;
+                    const size_t row =
+                        ((size_t)(d.row0 + node) * p.num_heads + d.kv_head * p.group +
+                         (tid - node * p.group)) * D;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32(o_column + c0, o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(poison ? NAN
+                                                   : none ? 0.f
+                                                          : __uint_as_float(o[k]) * inv);
+                        if (live)
+                            store_row32(p.out, p.out_dtype, row + c0, o);
+                        __syncwarp();
+                    }
+                } else {
+                    const size_t slot = (size_t)blockIdx.x * 2 + d.slot;
+                    float4 *acc = p.ws_acc + slot * (D / 4) * kTreeRows + tid;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld_x32(o_column + c0, o);
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                __stcg(acc + (size_t)(c0 / 4 + k) * kTreeRows,
+                                       make_float4(__uint_as_float(o[4 * k]),
+                                                   __uint_as_float(o[4 * k + 1]),
+                                                   __uint_as_float(o[4 * k + 2]),
+                                                   __uint_as_float(o[4 * k + 3])));
+                        }
+                        __syncwarp();
+                    }
+                    if (live) // l = -0: the row saw only scores of minus infinity
+                        __stcg(p.ws_ml + slot * kTreeRows + tid,
+                               make_float2(m, poison ? NAN : l == 0.f && saw ? -0.f : l));
+                }
+            }
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sh.o_free));
+        }
+    }
+    if (!ok)
+        report(p.dev_err, PA_DEVERR_TIMEOUT);
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tcgen05_fence_after();
+        tmem_dealloc(tmem, C::kColumns);
+    }
+}
+
+// Joins the parts of the unit that is cut before CTA blockIdx.x, if there is
+// one and no earlier cut in it: O = sum_p 2^(m_p - M) acc_p / sum_p
+// 2^(m_p - M) l_p. A thread has one row and D / 4 / gridDim.y columns of four.
+template <int D>
+__global__ void __launch_bounds__(kTreeRows) tree_merge_kernel(
     const __grid_constant__ TreeDecodeParams p)
 {
     pdl_launch_dependents();
     pdl_wait_prior_grid();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), r = blockIdx.x;
-    if (h >= p.num_heads)
+    const int b = blockIdx.x + 1;
+    const TreeMergeRecord rec = p.ws_records[b];
+    const int row = threadIdx.x;
+    if (rec.parts == 0 || row >= rec.rows)
         return;
-    const int limit = min(32 * p.mask_words, PA_TREE_MAX_NODES);
-    if (r == 0 && h == 0)
-        for (int k = lane; k < p.num_seqs; k += 32)
-            if (tree_span(p.tree_start, k, p.num_tokens, limit).size < 0)
-                report(p.dev_err, PA_DEVERR_TREE);
-    const int s = sequence_of_row(p, limit, r, lane);
-    if (s < 0)
-        return;
-    const TreeSpan t = tree_span(p.tree_start, s, p.num_tokens, limit);
-    const int bs = p.block_size, ctx = p.context_lens[s];
-    const int64_t capacity = min((int64_t)p.max_blocks_per_seq * bs, (int64_t)INT_MAX);
-    bool poison = false;
-    int n = 0;
-    if (ctx < 0 || (int64_t)ctx + t.size > capacity) {
-        report(p.dev_err, PA_DEVERR_CONTEXT_LEN);
-        poison = true;
-    } else {
-        n = ctx + t.size;
-    }
-    float q[E], acc[E];
-    const size_t row = ((size_t)r * p.num_heads + h) * D + lane * E;
-    for (int e = 0; e < E; ++e) {
-        q[e] = static_cast<float>(static_cast<const QT *>(p.query)[row + e]);
-        acc[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    bool any = false;
-    const int kvh = h / (p.num_heads / p.num_kv_heads);
-    const int32_t *words = p.mask + (size_t)r * p.mask_words;
-    for (int j = 0; j < n; ++j) {
-        const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + j / bs];
-        if (b < 0 || b >= p.num_blocks) {
-            report(p.dev_err, PA_DEVERR_BLOCK_ID);
-            poison = true;
-            continue;
+    const auto slot = [&](int i) { return i == 0 ? (size_t)(b - 1) * 2 + 1 : (size_t)(b + i - 1) * 2; };
+    float M = -INFINITY;
+    for (int i = 0; i < rec.parts; ++i)
+        M = fmaxf(M, __ldcg(p.ws_ml + slot(i) * kTreeRows + row).x);
+    const float use = M == -INFINITY ? 0.f : M;
+    constexpr int kCols = 4;
+    const int c0 = blockIdx.y * kCols;
+    float L = 0.f;
+    bool saw = false;
+    float4 o[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < rec.parts; ++i) {
+        const float2 ml = __ldcg(p.ws_ml + slot(i) * kTreeRows + row);
+        const float4 *acc = p.ws_acc + (slot(i) * (D / 4) + c0) * kTreeRows + row;
+        float4 a[kCols];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+            a[k] = __ldcg(acc + (size_t)k * kTreeRows);
+        const float w = ex2(ml.x - use);
+        saw |= ml.y != 0.f || signbit(ml.y);
+        L = fmaf(ml.y, w, L);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            o[k].x = fmaf(a[k].x, w, o[k].x);
+            o[k].y = fmaf(a[k].y, w, o[k].y);
+            o[k].z = fmaf(a[k].z, w, o[k].z);
+            o[k].w = fmaf(a[k].w, w, o[k].w);
         }
-        if (j >= ctx && !((words[(j - ctx) >> 5] >> ((j - ctx) & 31)) & 1))
-            continue;
-        any = true;
-        const int64_t tile = (int64_t)b * p.num_kv_heads + kvh;
-        float x[E], dot = 0.f;
-        TreeRow<T, D>::load(p.key_cache, tile, j % bs, bs, lane, x);
-        for (int e = 0; e < E; ++e)
-            dot = fmaf(q[e], x[e], dot);
-        for (int o = 16; o > 0; o >>= 1)
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        dot *= p.qk_scale_log2;
-        const float m_new = fmaxf(m, dot);
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        const float keep = exp2f(m - m_use), w = exp2f(dot - m_use);
-        TreeRow<T, D>::load(p.value_cache, tile, j % bs, bs, lane, x);
-        for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(w, x[e], acc[e] * keep);
-        l = fmaf(l, keep, w);
-        m = m_new;
     }
-    for (int e = 0; e < E; ++e)
-        store_out(p.out, p.out_dtype, row + e, poison ? NAN : any ? acc[e] / l : 0.f);
+    const bool none = L == 0.f && !saw;
+    const float inv = none ? 0.f : 1.f / L;
+    const int node = row / p.group;
+    const size_t at = ((size_t)(rec.first_row + node) * p.num_heads + rec.kv_head * p.group +
+                       (row - node * p.group)) * D + c0 * 4;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k)
+        store_row4(p.out, p.out_dtype, at + 4 * k,
+                   make_float4(none ? 0.f : o[k].x * inv, none ? 0.f : o[k].y * inv,
+                               none ? 0.f : o[k].z * inv, none ? 0.f : o[k].w * inv));
 }
 
 } // namespace pagedkv

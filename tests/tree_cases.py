@@ -179,13 +179,12 @@ class TreeBatch:
                 for r in range(t):
                     seen = ok[r]
                     out[a + r, h] = p[r, seen] @ vh[seen]
-                    if not torch.isfinite(out[a + r, h]).all():
-                        continue
+                    # Elements of a row that holds a NaN elsewhere have the same bound.
                     mag = p[r, seen] @ vh[seen].abs()
                     if seen.any():
                         d = (self.dim + 4) * 2.0 ** -24 * abs(scale) * \
                             (q[h][r].abs() @ kh[seen].abs().T).max()
-                        sub = n * 2.0 ** -25 * vh[seen].abs().max() \
+                        sub = n * 2.0 ** -25 * vh[seen].abs().nan_to_num(0, 0, 0).max() \
                             if self.io == torch.float16 else 0.0
                         room[a + r, h] = mag * (eps + 2 * d + 2.0 ** -20 + n * 2.0 ** -23) + sub
         return out, room
