@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstring>
 
 #include "pagedkv.h"
@@ -61,8 +62,11 @@ TreeWorkspace tree_workspace(int ctas, int head_dim)
     return w;
 }
 
+// Rows of a query box: half a tile where that is whole nodes.
+int tree_box_rows(int group) { return 64 % group == 0 ? 64 : kTreeRows / group * group; }
+
 // Query rows as (64 elements, heads, nodes, halves of a row): a box holds one
-// half of the group's heads of a tile's nodes, rows of 128 bytes in order.
+// half of the group's heads of some nodes, rows of 128 bytes in order.
 pa_status encode_tree_query(CUtensorMap *map, const void *query, int num_tokens, int num_heads,
                             int group, int head_dim)
 {
@@ -73,7 +77,7 @@ pa_status encode_tree_query(CUtensorMap *map, const void *query, int num_tokens,
     const cuuint64_t dims[4] = {64, (cuuint64_t)num_heads, (cuuint64_t)num_tokens,
                                 (cuuint64_t)head_dim / 64};
     const cuuint64_t strides[3] = {row, row * num_heads, 128};
-    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)(kTreeRows / group), 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)(tree_box_rows(group) / group), 1};
     const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(query), dims,
                            strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -118,7 +122,7 @@ pa_status launch_tree(const TreeTmaParams &g, int ctas, cudaStream_t st)
     e = launch_pdl(kernel, dim3(ctas), dim3(C::kThreads), C::kSmem, st, g);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_decode launch");
-    e = launch_pdl(tree_merge_kernel<D>, dim3(ctas - 1, D / 16), dim3(kTreeRows), 0, st, g.p);
+    e = launch_pdl(tree_merge_kernel<D>, dim3(ctas - 1, D / 4 / kMergeCols), dim3(kTreeRows), 0, st, g.p);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_merge launch");
     return ok();
@@ -286,7 +290,10 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.mask_words = mask_words;
     p.out_dtype = (int32_t)out_dtype;
-    p.qk_scale_log2 = scale * 1.4426950408889634f;
+    p.q_box_rows = tree_box_rows(p.group);
+    // Never zero: a masked score is -infinity times this. The smallest normal
+    // number makes every finite score as equal as zero would.
+    p.qk_scale_log2 = scale == 0.f ? FLT_MIN : scale * 1.4426950408889634f;
     if ((s = encode_tree_query(&g.q, query, num_tokens, num_heads, p.group, cache->head_dim)) !=
             PA_OK ||
         (s = encode_tree_pool(&g.k, key_cache, cache)) != PA_OK ||

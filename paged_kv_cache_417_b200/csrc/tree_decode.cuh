@@ -17,8 +17,10 @@
 //
 // Roles of a CTA's warps:
 //   0-3  one thread per row: softmax, and the rescaling and writing of rows
-//   4    fetches Q, K and V by TMA, block by block through the block table
-//   5    issues the MMAs: S = Q K^T (128 x 64, both operands in shared
+//   4, 5 fetch Q and K, and V, by TMA, block by block through the block table
+//        (one warp for both took 1.5k of the 2.6k cycles of a tile to issue
+//        its copies, and held K of the next tile back behind V of this one)
+//   6    issues the MMAs: S = Q K^T (128 x 64, both operands in shared
 //        memory) and O += P V (128 x D, P in tensor memory)
 // Tensor memory (256 columns a CTA): O in D fp32 columns and two S tiles of
 // 64; P, 16 bits, overwrites the S tile it comes from. S of the next tile is
@@ -34,11 +36,11 @@
 //
 // Masks. A tile that ends before the context does is seen by every row. Tiles
 // at and behind the context's end take the slower path: scores that a row
-// does not see are replaced before the maximum and their weights by zero. A
-// product 0 * NaN would still reach a row, so V rows behind the last token
-// are zeroed in shared memory, and a tree node's V row that holds a NaN or an
-// infinity is taken out of the tile and added to the rows that see it one by
-// one (rescue_rows).
+// does not see become minus infinity (plus, for a negative scale). A product
+// 0 * NaN would still reach a row, so in those tiles the V rows of nodes and
+// behind the last token are looked through, and one that holds a NaN or an
+// infinity is zeroed in shared memory and, if it is a node's, added to the
+// rows that see it one by one (rescue_rows).
 //
 // Layouts. K and V blocks lie in shared memory as [8-row group][64-element
 // half][8 rows][128 bytes], swizzled, which one 4-D box per block fetches
@@ -62,6 +64,11 @@ namespace pagedkv {
 constexpr int kTreeRows = 128;  // rows of a tile: the MMA's M
 constexpr int kTreeTile = 64;   // tokens of a tile
 constexpr int kTreeCtasPerSm = 2;
+constexpr int kSoftmaxWarps = 4;
+#ifndef PA_TREE_UNIT_COST
+#define PA_TREE_UNIT_COST 4
+#endif
+constexpr int kTreeUnitCost = PA_TREE_UNIT_COST;
 constexpr float kTreeSlack = 6.f;
 constexpr float kTreeBias = 8.f;
 
@@ -84,6 +91,7 @@ struct TreeDecodeParams {
     float2 *ws_ml;               // [CTAs][2][kTreeRows] = (m, l)
     int32_t num_seqs, num_tokens, num_heads, num_kv_heads, group, num_blocks;
     int32_t max_blocks_per_seq, mask_words, out_dtype;
+    int32_t q_box_rows; // rows of a query box: 64 where the group divides it
     float qk_scale_log2;
 };
 
@@ -124,22 +132,43 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeDecodeParams &p, int s, in
     return q;
 }
 
-__device__ __forceinline__ int64_t tree_seq_tiles(const TreeDecodeParams &p, const TreeSeq &q)
+__device__ __forceinline__ int64_t tree_seq_places(const TreeDecodeParams &p, const TreeSeq &q)
 {
-    return (int64_t)q.tiles * q.row_tiles * p.num_kv_heads;
+    return (int64_t)(q.tiles + kTreeUnitCost) * q.row_tiles * p.num_kv_heads;
 }
 
-// What a CTA does: its tiles, and where they begin. Of n = `ctas` pieces of
-// the line, piece b begins at b * total / n.
+// What a CTA does. The line has kTreeUnitCost + tiles places per unit, and of
+// n = `ctas` pieces piece b begins at place b * total / n: the first
+// kTreeUnitCost places of a unit stand for its fixed cost (query rows, the
+// masked tiles at its end, the epilogue), so that a piece of many short units
+// takes as long as one of a few long ones. A piece that begins in them begins
+// with the unit's first tile.
 struct TreePlan {
-    int64_t begin, end;   // of the line
-    int64_t seq_begin;    // first tile of sequence `seq`
-    int64_t each;         // total / ctas
-    int32_t seq, ctas, rest; // rest: total % ctas
+    int64_t begin, end;      // places of the line
+    int64_t each;            // total / ctas
+    int32_t ctas, rest;      // rest: total % ctas
+    int64_t unit_begin;      // first place of the unit that `begin` is in
+    int32_t seq, unit, tile; // that unit, and the piece's first tile of it
+    bool empty;              // no tile in this piece
 
     __device__ __forceinline__ int64_t piece(int b) const
     {
         return b * each + (uint32_t)(b * rest) / (uint32_t)ctas;
+    }
+    // The end of this piece among the tiles of a unit.
+    __device__ __forceinline__ int tile_end(int64_t first_place, int tiles) const
+    {
+        return (int)max((int64_t)0, min((int64_t)tiles, end - first_place - kTreeUnitCost));
+    }
+    // The thread whose sequence q, beginning at `first`, holds `begin`.
+    __device__ __forceinline__ void locate(const TreeSeq &q, int s, int64_t first)
+    {
+        const int places = q.tiles + kTreeUnitCost;
+        seq = s;
+        unit = (int)((begin - first) / places);
+        unit_begin = first + (int64_t)unit * places;
+        tile = max(0, (int)(begin - unit_begin) - kTreeUnitCost);
+        empty = tile_end(unit_begin, q.tiles) <= tile;
     }
 };
 
@@ -153,12 +182,13 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
     const bool one = p.num_seqs <= (int)blockDim.x; // the usual case: one sequence per thread
     int64_t total = 0, mine = 0, before = 0;
     int32_t error = 0;
+    TreeSeq q;
     for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
         const int s = s0 + tid;
         if (s < p.num_seqs) {
-            const TreeSeq q = tree_seq(p, s, bs);
+            q = tree_seq(p, s, bs);
             error |= q.error;
-            mine = tree_seq_tiles(p, q);
+            mine = tree_seq_places(p, q);
             total += mine;
         }
     }
@@ -182,7 +212,7 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
     const int ctas = (int)min((int64_t)gridDim.x, total);
     if (tid == 0) {
         plan->ctas = ctas;
-        plan->begin = plan->end = 0;
+        plan->empty = true;
         if ((int)blockIdx.x < ctas) {
             plan->each = total / ctas;
             plan->rest = (int)(total % ctas);
@@ -197,8 +227,7 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
     if (one) {
         const int64_t first = before + upto - mine;
         if (mine > 0 && first <= begin && begin < first + mine) {
-            plan->seq = tid;
-            plan->seq_begin = first;
+            plan->locate(q, tid, first);
         }
         __syncthreads();
         return;
@@ -207,8 +236,10 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
     int64_t base = 0;
     for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
         mine = 0;
-        if (s0 + tid < p.num_seqs)
-            mine = tree_seq_tiles(p, tree_seq(p, s0 + tid, bs));
+        if (s0 + tid < p.num_seqs) {
+            q = tree_seq(p, s0 + tid, bs);
+            mine = tree_seq_places(p, q);
+        }
         upto = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -227,8 +258,7 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
         }
         const int64_t first = base + before + upto - mine;
         if (mine > 0 && first <= begin && begin < first + mine) {
-            plan->seq = s0 + tid;
-            plan->seq_begin = first;
+            plan->locate(q, s0 + tid, first);
         }
         base += chunk;
         if (base > begin)
@@ -245,6 +275,7 @@ struct TreeSegment {
     int32_t rows;         // live rows of the tile
     int32_t kv_head;
     int32_t slot;         // -1: writes its rows; 0, 1: leaves a part in that slot
+    int32_t q_at;         // byte offset of its query rows in the query area
     int32_t last;         // 1: the CTA's last segment
 };
 
@@ -256,7 +287,7 @@ template <typename T, int D, int BS> struct TreeCfg {
     static constexpr int kStages = D == 128 ? 2 : 4;           // of K and of V
     static constexpr int kBlocks = kTreeTile / BS;             // blocks of a tile
     static constexpr int kBlockBytes = BS * D * 2;
-    static constexpr int kThreads = 192;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
     static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
     static constexpr uint32_t kColumns = 256;
     static constexpr uint32_t kS0 = D; // tensor-memory column of the first S tile
@@ -265,8 +296,8 @@ template <typename T, int D, int BS> struct TreeCfg {
 // Barriers and small state of a CTA.
 template <int NS> struct TreeShared {
     uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-    // q_full twice: the fetching warp may be two segments ahead of the softmax.
-    uint64_t q_full[2], q_empty, s_full[2], p_full[2], o_full, o_free, warps, drain;
+    // By segment; q_empty by its parity.
+    uint64_t d_full[4], q_full[4], q_empty[2], s_full[2], p_full[2], o_full, o_free, warps, drain;
     TreePlan plan;
     int64_t sums[32];
     TreeSegment seg[4];
@@ -301,38 +332,57 @@ template <int D> __device__ __forceinline__ uint32_t tree_piece_at(int j, int c)
            (((c & 7) ^ (j & 7)) << 4);
 }
 
-// Which of the 64 tokens from `t0` on a row sees: those before the context's
-// end, then those whose bit is set in its mask row.
-__device__ __forceinline__ uint64_t tree_seen(const int32_t *words, int num_words, int t0, int ctx,
-                                              int n)
-{
-    const int b0 = t0 - ctx; // node of column 0; negative: cached tokens first
-    uint64_t bits;
-    const auto word = [&](int w) -> uint32_t {
-        return w < num_words ? (uint32_t)words[w] : 0u;
-    };
-    if (b0 >= 0) {
-        const int w = b0 >> 5, sh = b0 & 31;
-        const uint32_t a = word(w), b = word(w + 1), c = sh ? word(w + 2) : 0u;
-        bits = (uint64_t)__funnelshift_r(a, b, sh) | ((uint64_t)__funnelshift_r(b, c, sh) << 32);
-    } else if (b0 > -kTreeTile) {
-        bits = (((uint64_t)word(1) << 32 | word(0)) << -b0) | ((1ull << -b0) - 1);
-    } else {
-        bits = ~0ull;
+// Which of the 64 tokens of a tile a row sees: those before the context's
+// end, then those whose bit is set in its mask row. The words are loaded
+// ahead of their use.
+struct TreeSeen {
+    uint32_t w[3];
+    __device__ __forceinline__ void load(const int32_t *words, int num_words, int t0, int ctx)
+    {
+        const int first = max(t0 - ctx, 0) >> 5;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            w[k] = first + k < num_words ? (uint32_t)words[first + k] : 0u;
     }
-    if (n - t0 < kTreeTile)
-        bits &= n > t0 ? (1ull << (n - t0)) - 1 : 0ull;
-    return bits;
+    __device__ __forceinline__ uint64_t bits(int t0, int ctx, int n) const
+    {
+        const int b0 = t0 - ctx; // node of column 0; negative: cached tokens first
+        uint64_t b = ~0ull;
+        if (b0 >= 0)
+            b = (uint64_t)__funnelshift_r(w[0], w[1], b0) |
+                ((uint64_t)__funnelshift_r(w[1], w[2], b0) << 32);
+        else if (b0 > -kTreeTile)
+            b = (((uint64_t)w[1] << 32 | w[0]) << -b0) | ((1ull << -b0) - 1);
+        if (n - t0 < kTreeTile)
+            b &= n > t0 ? (1ull << (n - t0)) - 1 : 0ull;
+        return b;
+    }
+};
+
+// 32 bytes to 32-byte (wide) or 16-byte aligned memory.
+__device__ __forceinline__ void store32(void *to, const uint32_t *w, bool wide)
+{
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                     "r"(w[7])
+                     : "memory");
+    else {
+        static_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
-// 32 (4) consecutive floats of a row to `out`, rounded to its type.
+// 32 (4) consecutive floats of a row to `out`, rounded to its type. A thread
+// per row makes every store of a warp touch 32 lines, so each takes a whole
+// sector where `out` is aligned to one.
 __device__ __forceinline__ void store_row32(void *out, int dtype, size_t at, const uint32_t (&o)[32])
 {
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     if (dtype == 2) {
-        uint4 *to = reinterpret_cast<uint4 *>(static_cast<float *>(out) + at);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int k = 0; k < 32; k += 8)
+            store32(static_cast<float *>(out) + at + k, o + k, wide);
         return;
     }
     uint32_t w[16];
@@ -341,10 +391,9 @@ __device__ __forceinline__ void store_row32(void *out, int dtype, size_t at, con
         const float a = __uint_as_float(o[2 * k]), b = __uint_as_float(o[2 * k + 1]);
         w[k] = dtype == 0 ? pack2<__half>(a, b) : pack2<__nv_bfloat16>(a, b);
     }
-    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        to[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int k = 0; k < 16; k += 8)
+        store32(static_cast<uint16_t *>(out) + at + 2 * k, w + k, wide);
 }
 
 __device__ __forceinline__ void store_row4(void *out, int dtype, size_t at, float4 v)
@@ -408,6 +457,139 @@ template <typename QT> __device__ __forceinline__ bool not_finite(const uint4 &x
     return bad;
 }
 
+// The fetching warps: K tiles of the CTA's piece, with each segment's
+// description and query rows, or its V tiles.
+template <typename QT, int D, int BS, bool kIsV>
+__device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
+                                           TreeShared<TreeCfg<QT, D, BS>::kStages> &sh,
+                                           uint32_t q_tile, uint32_t ring, bool &ok)
+{
+    using C = TreeCfg<QT, D, BS>;
+    constexpr int NS = C::kStages;
+    const TreeDecodeParams &p = g.p;
+    const int lane = threadIdx.x & 31, per_tile = kTreeRows / p.group;
+    const auto wait = [&](uint64_t &bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu,
+                        ok && mbar_wait_suspended(smem_addr(&bar), parity, kWaitLimitNs));
+        return ok;
+    };
+    uint64_t *full = kIsV ? sh.v_full : sh.k_full, *empty = kIsV ? sh.v_empty : sh.k_empty;
+    const CUtensorMap *map = kIsV ? &g.v : &g.k;
+    int s = sh.plan.seq;
+    TreeSeq q = tree_seq(p, s, BS);
+    int64_t unit_begin = sh.plan.unit_begin;
+    int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
+    uint32_t q_seen[2] = {0, 0}; // segments of each parity whose query rows were seen done
+    bool was_whole = false;
+    for (bool last = false; !last && ok; ++seg) {
+        const int rt = unit % q.row_tiles, h = unit / q.row_tiles;
+        const int tile0 = tile, end = sh.plan.tile_end(unit_begin, q.tiles);
+        unit_begin += q.tiles + kTreeUnitCost;
+        last = sh.plan.end <= unit_begin + kTreeUnitCost; // no tile of the next unit
+        const int n = q.bad_context ? 0 : q.ctx + q.nodes;
+        const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+        const auto block_id = [&](int t) { // lane's block of tile t, -1: none
+            const int b = t * C::kBlocks + lane;
+            return lane < C::kBlocks && b * BS < n ? table[b] : -1;
+        };
+        int id = block_id(tile);
+        for (; tile < end; ++tile, ++it) {
+            const int st = it % NS;
+            const uint32_t ph = (it / NS) & 1;
+            const int left = n - tile * kTreeTile; // tokens from here on
+            const int blocks = left <= 0 ? 0 : min(C::kBlocks, (left + BS - 1) / BS);
+            const int next = tile + 1 < end ? block_id(tile + 1) : -1;
+            if (it >= NS && !wait(empty[st], ph ^ 1))
+                break;
+            // Only now, so that the table's latency passes during the wait.
+            const bool bad = lane < blocks && (id < 0 || id >= p.num_blocks);
+            const bool any_bad = __any_sync(0xffffffffu, bad);
+            const int row8 = (int)((((int64_t)(bad ? 0 : id) * p.num_kv_heads + h) * BS) >> 3);
+            const uint32_t bar = smem_addr(&full[st]), to = ring + st * C::kTileBytes;
+            if (elect_one()) {
+                if (kIsV && tile == tile0)
+                    sh.poison[seg & 3] = q.bad_context;
+                if (any_bad) {
+                    report(p.dev_err, PA_DEVERR_BLOCK_ID);
+                    if (kIsV)
+                        sh.poison[seg & 3] = 1;
+                }
+                mbar_arrive_expect_tx(bar, blocks * C::kBlockBytes);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < C::kBlocks; ++b) {
+                const int y = __shfl_sync(0xffffffffu, row8, b);
+                if (b < blocks && elect_one())
+                    tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, y, bar);
+                __syncwarp();
+            }
+            if (!kIsV && tile == tile0) {
+                // A segment of up to 64 rows takes half of the query area,
+                // so that its rows can come while the last segment's are
+                // still multiplied; a larger one takes all of it.
+                const int rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
+                const bool whole = rows > 64 || p.q_box_rows != 64;
+                const auto q_free = [&](int of) { // segment `of`'s rows are done with
+                    if (of >= 0 && (q_seen[of & 1] <= of >> 1))
+                        return wait(sh.q_empty[of & 1], q_seen[of & 1]++ & 1);
+                    return true;
+                };
+                if (!q_free(seg - 2) || ((whole || was_whole) && !q_free(seg - 1)))
+                    break;
+                was_whole = whole;
+                if (elect_one()) {
+                    TreeSegment d;
+                    d.tile0 = tile0;
+                    d.tile1 = end;
+                    d.ctx = q.bad_context ? 0 : q.ctx;
+                    d.n = n;
+                    d.row0 = q.first + rt * per_tile;
+                    d.rows = rows;
+                    d.kv_head = h;
+                    d.slot = tile0 > 0 ? 0 : end < q.tiles ? 1 : -1;
+                    d.q_at = whole ? 0 : (seg & 1) * 8192;
+                    d.last = last;
+                    sh.seg[seg & 3] = d;
+                    mbar_arrive(smem_addr(&sh.d_full[seg & 3]));
+                    const uint32_t qbar = smem_addr(&sh.q_full[seg & 3]);
+                    const int boxes = p.q_box_rows == 64 && rows > 64 ? 2 : 1;
+                    mbar_arrive_expect_tx(qbar, boxes * p.q_box_rows * 128 * C::kHalves);
+                    for (int b = 0; b < boxes; ++b)
+                        for (int u = 0; u < C::kHalves; ++u)
+                            tma_load_4d(q_tile + d.q_at + u * (kTreeRows * 128) + b * 8192, &g.q,
+                                        0, h * p.group, d.row0 + b * (64 / p.group), u, qbar);
+                }
+                __syncwarp();
+            }
+            id = next;
+        }
+        if (!ok)
+            break;
+        // The next unit: of this sequence, or of the next one with any.
+        tile = 0;
+        if (++unit == q.row_tiles * p.num_kv_heads && !last) {
+            unit = 0;
+            for (++s; s < p.num_seqs; s += 32) {
+                const bool has = s + lane < p.num_seqs && tree_seq(p, s + lane, BS).nodes > 0;
+                const unsigned hit = __ballot_sync(0xffffffffu, has);
+                if (hit) {
+                    s += __ffs(hit) - 1;
+                    break;
+                }
+            }
+            q = tree_seq(p, s, BS);
+        }
+    }
+    if (!ok) { // let the copies in flight land before the CTA goes
+        constexpr uint64_t kDrainNs = 10000000;
+        for (int i = max(0, it - NS + 1); i <= it; ++i)
+            mbar_wait_bounded(smem_addr(&full[i % NS]), (i / NS) & 1, kDrainNs);
+        if (!kIsV)
+            mbar_wait_bounded(smem_addr(&sh.q_full[seg & 3]), (seg >> 2) & 1, kDrainNs);
+    }
+}
+
 template <typename QT, int D, int BS>
 __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
     tree_decode_tc_kernel(const __grid_constant__ TreeTmaParams g)
@@ -431,213 +613,125 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
             mbar_init(smem_addr(&sh.v_full[i]), 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 1);
         }
-        mbar_init(smem_addr(&sh.q_empty), 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&sh.d_full[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.q_empty[i]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i]), 4); // one per softmax warp
+            mbar_init(smem_addr(&sh.p_full[i]), kSoftmaxWarps);
         }
         mbar_init(smem_addr(&sh.o_full), 1);
-        mbar_init(smem_addr(&sh.o_free), 4);
-        mbar_init(smem_addr(&sh.warps), 4);
+        mbar_init(smem_addr(&sh.o_free), kSoftmaxWarps);
+        mbar_init(smem_addr(&sh.warps), kSoftmaxWarps);
         mbar_init(smem_addr(&sh.drain), 1);
         fence_mbar_init();
         sh.keep_o = -1;
         sh.strange[0] = sh.strange[1] = 0;
     }
-    if (warp == 5)
+    if (warp == kSoftmaxWarps + 2)
         tmem_alloc(smem_addr(&sh.tmem), C::kColumns);
     tcgen05_fence_before();
     pdl_wait_prior_grid();
     tree_plan(p, BS, &sh.plan, sh.sums);
     tcgen05_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int count = (int)min(sh.plan.end - sh.plan.begin, (int64_t)INT_MAX); // tiles of the CTA
     bool ok = true;
     const auto wait = [&](uint64_t &bar, uint32_t parity) {
-        ok = ok && mbar_wait_bounded(smem_addr(&bar), parity, kWaitLimitNs);
+        ok = ok && mbar_wait_suspended(smem_addr(&bar), parity, kWaitLimitNs);
         return ok;
     };
 
-    if (count == 0) {
+    if (sh.plan.empty) {
         if (tid == 0)
             p.ws_records[blockIdx.x].parts = 0;
-    } else if (warp == 4) {
-        // --- fetch: segments, and the tiles of each ----------------------------------------
-        int s = sh.plan.seq;
-        TreeSeq q = tree_seq(p, s, BS);
-        int64_t into = sh.plan.begin - sh.plan.seq_begin; // tile of the sequence
-        int unit = (int)(into / q.tiles), tile = (int)(into - (int64_t)unit * q.tiles);
-        const int per_tile = kTreeRows / p.group;
-        int it = 0, segs = 0;
-        for (int seg = 0; it < count && ok; ++seg) {
-            segs = seg;
-            const int rt = unit % q.row_tiles, h = unit / q.row_tiles;
-            const int end = min(q.tiles, tile + count - it);
-            const int n = q.bad_context ? 0 : q.ctx + q.nodes;
-            const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-            const auto block_id = [&](int t) { // lane's block of tile t, -1: none
-                const int b = t * C::kBlocks + lane;
-                return lane < C::kBlocks && b * BS < n ? table[b] : -1;
-            };
-            int id = block_id(tile);
-            for (const int tile0 = tile; tile < end && ok; ++tile, ++it) {
-                const int st = it % NS;
-                const uint32_t ph = (it / NS) & 1;
-                const int left = n - tile * kTreeTile; // tokens from here on
-                const int blocks = left <= 0 ? 0 : min(C::kBlocks, (left + BS - 1) / BS);
-                const int next = tile + 1 < end ? block_id(tile + 1) : -1;
-                const bool here = lane < blocks;
-                const bool bad = here && (id < 0 || id >= p.num_blocks);
-                const bool any_bad = __any_sync(0xffffffffu, bad);
-                const int64_t row8 =
-                    (((int64_t)(bad ? 0 : id) * p.num_kv_heads + h) * BS) >> 3;
-                if (it >= NS)
-                    wait(sh.k_empty[st], ph ^ 1);
-                if (lane == 0 && ok) {
-                    if (tile == tile0) {
-                        sh.poison[seg & 3] = q.bad_context;
-                    }
-                    if (any_bad) {
-                        report(p.dev_err, PA_DEVERR_BLOCK_ID);
-                        sh.poison[seg & 3] = 1;
-                    }
-                    mbar_arrive_expect_tx(smem_addr(&sh.k_full[st]), blocks * C::kBlockBytes);
-                }
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                if (here)
-                    tma_load_4d(k_tiles + st * C::kTileBytes + lane * C::kBlockBytes, &g.k, 0, 0,
-                                0, (int)row8, smem_addr(&sh.k_full[st]));
-                if (tile == tile0) {
-                    if (seg > 0)
-                        wait(sh.q_empty, (seg - 1) & 1);
-                    if (lane == 0 && ok) {
-                        TreeSegment d;
-                        d.tile0 = tile0;
-                        d.tile1 = end;
-                        d.ctx = q.bad_context ? 0 : q.ctx;
-                        d.n = n;
-                        d.row0 = q.first + rt * per_tile;
-                        d.rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
-                        d.kv_head = h;
-                        d.slot = tile0 > 0 ? 0 : end < q.tiles ? 1 : -1;
-                        d.last = it + end - tile0 >= count;
-                        sh.seg[seg & 3] = d;
-                        const int bytes = per_tile * p.group * 128;
-                        mbar_arrive_expect_tx(smem_addr(&sh.q_full[seg & 1]), bytes * C::kHalves);
-                        for (int u = 0; u < C::kHalves; ++u)
-                            tma_load_4d(q_tile + u * (kTreeRows * 128), &g.q, 0, h * p.group,
-                                        d.row0, u, smem_addr(&sh.q_full[seg & 1]));
-                    }
-                }
-                if (it >= NS)
-                    wait(sh.v_empty[st], ph ^ 1);
-                if (lane == 0 && ok)
-                    mbar_arrive_expect_tx(smem_addr(&sh.v_full[st]), blocks * C::kBlockBytes);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                if (here)
-                    tma_load_4d(v_tiles + st * C::kTileBytes + lane * C::kBlockBytes, &g.v, 0, 0,
-                                0, (int)row8, smem_addr(&sh.v_full[st]));
-                id = next;
-            }
-            // The next unit: of this sequence, or of the next one with any.
-            tile = 0;
-            if (++unit == q.row_tiles * p.num_kv_heads && it < count) {
-                unit = 0;
-                for (++s; s < p.num_seqs; s += 32) {
-                    const bool has = s + lane < p.num_seqs && tree_seq(p, s + lane, BS).nodes > 0;
-                    const unsigned hit = __ballot_sync(0xffffffffu, has);
-                    if (hit) {
-                        s += __ffs(hit) - 1;
-                        break;
-                    }
-                }
-                q = tree_seq(p, s, BS);
-            }
-        }
-        if (!ok) { // let the copies in flight land before the CTA goes
-            constexpr uint64_t kDrainNs = 10000000;
-            for (int i = max(0, it - NS + 1); i <= it; ++i) {
-                mbar_wait_bounded(smem_addr(&sh.k_full[i % NS]), (i / NS) & 1, kDrainNs);
-                mbar_wait_bounded(smem_addr(&sh.v_full[i % NS]), (i / NS) & 1, kDrainNs);
-            }
-            mbar_wait_bounded(smem_addr(&sh.q_full[segs & 1]), (segs >> 1) & 1, kDrainNs);
-        }
-    } else if (warp == 5) {
-        // --- MMAs, one thread ---------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kIdescQk = umma_idesc(kBf16, false, kTreeRows, kTreeTile);
-            constexpr uint32_t kIdescPv = umma_idesc(kBf16, true, kTreeRows, D);
-            int it = 0, pending = -1; // tile whose P V is still to be issued
-            bool pending_first = false;
-            int seg = -1, seg_end = 0, segments_read = 0;
-            const auto issue_pv = [&]() {
-                const int st = pending % NS;
-                wait(sh.p_full[pending & 1], (pending >> 1) & 1);
-                wait(sh.v_full[st], (pending / NS) & 1);
-                bool add = !pending_first;
-                if (pending_first) {
-                    if (segments_read > 0)
-                        wait(sh.o_free, (segments_read - 1) & 1);
-                    ++segments_read;
-                    add = *(volatile int32_t *)&sh.keep_o == pending;
-                }
-                if (!ok)
+    } else if (warp == kSoftmaxWarps) {
+        tree_fetch<QT, D, BS, false>(g, sh, q_tile, k_tiles, ok);
+    } else if (warp == kSoftmaxWarps + 1) {
+        tree_fetch<QT, D, BS, true>(g, sh, q_tile, v_tiles, ok);
+    } else if (warp == kSoftmaxWarps + 2) {
+        // --- MMAs: the warp waits together, one lane issues ---------------------------------
+        constexpr uint32_t kIdescQk = umma_idesc(kBf16, false, kTreeRows, kTreeTile);
+        constexpr uint32_t kIdescPv = umma_idesc(kBf16, true, kTreeRows, D);
+        const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, wait(bar, parity));
+            return ok;
+        };
+        int pending = -1; // tile whose P V is still to be issued
+        bool pending_first = false, last = false;
+        int segments_read = 0;
+        uint32_t q_at = q_tile;
+        const auto issue_pv = [&]() {
+            const int st = pending % NS;
+            if (!wait_warp(sh.p_full[pending & 1], (pending >> 1) & 1) ||
+                !wait_warp(sh.v_full[st], (pending / NS) & 1))
+                return;
+            bool add = !pending_first;
+            if (pending_first) {
+                if (segments_read > 0 && !wait_warp(sh.o_free, (segments_read - 1) & 1))
                     return;
-                tcgen05_fence_after();
-                const uint32_t v = v_tiles + st * C::kTileBytes;
-                const uint32_t a = tmem + C::kS0 + (pending & 1) * kTreeTile;
+                ++segments_read;
+                add = *(volatile int32_t *)&sh.keep_o == pending;
+            }
+            tcgen05_fence_after();
+            const uint64_t v = umma_desc(v_tiles + st * C::kTileBytes, 1024, C::kGroupBytes);
+            const uint32_t a = tmem + C::kS0 + (pending & 1) * kTreeTile;
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kTreeTile / 16; ++k)
-                    tcgen05_mma_ts(tmem, a + k * 8,
-                                   umma_desc(v + k * 2 * C::kGroupBytes, 1024, C::kGroupBytes),
-                                   kIdescPv, add || k > 0);
+                    tcgen05_mma_ts(tmem, a + k * 8, v + (k * 2 * C::kGroupBytes >> 4), kIdescPv,
+                                   add || k > 0);
                 tcgen05_commit(smem_addr(&sh.v_empty[st]));
                 tcgen05_commit(smem_addr(&sh.o_full));
-                pending = -1;
-            };
-            for (; it < count && ok; ++it) {
-                const bool first = it == seg_end;
-                if (first) {
+            }
+            __syncwarp();
+            pending = -1;
+        };
+        for (int it = 0, seg = -1, seg_end = 0; ok; ++it) {
+            const bool first = it == seg_end;
+            if (first) {
+                if (last) {
                     if (pending >= 0)
                         issue_pv();
-                    ++seg;
-                    if (!wait(sh.q_full[seg & 1], (seg >> 1) & 1))
-                        break;
-                    seg_end = it + sh.seg[seg & 3].tile1 - sh.seg[seg & 3].tile0;
-                }
-                const int st = it % NS;
-                if (!wait(sh.k_full[st], (it / NS) & 1))
                     break;
-                tcgen05_fence_after();
-                const uint32_t k0 = k_tiles + st * C::kTileBytes;
+                }
+                ++seg;
+                if (!wait_warp(sh.q_full[seg & 3], (seg >> 2) & 1))
+                    break;
+                const TreeSegment &d = sh.seg[seg & 3];
+                seg_end = it + d.tile1 - d.tile0;
+                last = d.last;
+                q_at = q_tile + d.q_at;
+            }
+            const int st = it % NS;
+            if (!wait_warp(sh.k_full[st], (it / NS) & 1))
+                break;
+            tcgen05_fence_after();
+            const uint64_t q0 = umma_desc(q_at, 16, 1024);
+            const uint64_t k0 = umma_desc(k_tiles + st * C::kTileBytes, 16, C::kGroupBytes);
+            const uint32_t s_tile = tmem + C::kS0 + (it & 1) * kTreeTile;
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tcgen05_mma_ss(tmem + C::kS0 + (it & 1) * kTreeTile,
-                                   umma_desc(q_tile + (k / 4) * (kTreeRows * 128) + (k % 4) * 32,
-                                             16, 1024),
-                                   umma_desc(k0 + (k / 4) * 1024 + (k % 4) * 32, 16,
-                                             C::kGroupBytes),
-                                   kIdescQk, k > 0);
+                    tcgen05_mma_ss(s_tile, q0 + (((k / 4) * (kTreeRows * 128) + (k % 4) * 32) >> 4),
+                                   k0 + (((k / 4) * 1024 + (k % 4) * 32) >> 4), kIdescQk, k > 0);
                 tcgen05_commit(smem_addr(&sh.s_full[it & 1]));
                 tcgen05_commit(smem_addr(&sh.k_empty[st]));
                 if (it + 1 == seg_end)
-                    tcgen05_commit(smem_addr(&sh.q_empty));
-                if (pending >= 0)
-                    issue_pv();
-                pending = it;
-                pending_first = first;
+                    tcgen05_commit(smem_addr(&sh.q_empty[seg & 1]));
             }
-            if (ok && pending >= 0)
+            __syncwarp();
+            if (pending >= 0)
                 issue_pv();
-            if (!ok) { // MMAs in flight read shared memory and write tensor memory
+            pending = it;
+            pending_first = first;
+        }
+        if (!ok) { // MMAs in flight read shared memory and write tensor memory
+            if (elect_one())
                 tcgen05_commit(smem_addr(&sh.drain));
-                mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitLimitNs);
-            }
+            __syncwarp();
+            mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitLimitNs);
         }
     } else {
         // --- softmax, one thread per row ----------------------------------------------------
@@ -659,12 +753,10 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
         if (tid == 0) {
             // The unit that this piece begins inside of, if it was cut here first.
             const TreePlan &plan = sh.plan;
-            const TreeSeq q = tree_seq(p, plan.seq, BS);
-            const int64_t into = plan.begin - plan.seq_begin;
-            const int unit = (int)(into / q.tiles), tile = (int)(into - (int64_t)unit * q.tiles);
-            const int64_t unit_begin = plan.begin - tile, unit_last = unit_begin + q.tiles - 1;
             TreeMergeRecord rec = {0, 0, 0, 0};
-            if (tile > 0 && unit_begin >= plan.piece(blockIdx.x - 1)) {
+            if (plan.tile > 0 && plan.piece(blockIdx.x - 1) <= plan.unit_begin + kTreeUnitCost) {
+                const TreeSeq q = tree_seq(p, plan.seq, BS);
+                const int64_t unit_last = plan.unit_begin + kTreeUnitCost + q.tiles - 1;
                 int e = blockIdx.x, hi = plan.ctas - 1; // the CTA with the unit's last tile
                 while (e < hi) {
                     const int mid = (e + hi + 1) / 2;
@@ -673,36 +765,46 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                     else
                         hi = mid - 1;
                 }
-                const int per_tile = kTreeRows / p.group, rt = unit % q.row_tiles;
+                const int per_tile = kTreeRows / p.group, rt = plan.unit % q.row_tiles;
                 rec.parts = e - (int)blockIdx.x + 2;
                 rec.rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
                 rec.first_row = q.first + rt * per_tile;
-                rec.kv_head = unit / q.row_tiles;
+                rec.kv_head = plan.unit / q.row_tiles;
             }
             p.ws_records[blockIdx.x] = rec;
         }
         __syncwarp();
+        const int node = tid / p.group; // of the tile
         int it = 0;
-        bool more = true;
-        for (int seg = 0; more && ok; ++seg) {
-            if (!wait_warp(sh.q_full[seg & 1], (seg >> 1) & 1))
-                break;
-            const TreeSegment d = sh.seg[seg & 3];
-            more = !d.last;
-            const int node = tid / p.group; // of the tile
-            const bool live = tid < d.rows;
-            const bool warp_live = warp * 32 < d.rows;
-            const int32_t *words =
-                p.mask + (size_t)(d.row0 + (live ? node : 0)) * p.mask_words;
+        TreeSegment d, d_next; // this segment, and the next once it is known
+        TreeSeen ahead;        // mask words of the next masked tile
+        bool live = false;
+        const int32_t *words = nullptr;
+        const auto masked = [&](const TreeSegment &of, int tile) {
+            return (tile + 1) * kTreeTile > of.ctx;
+        };
+        const auto look_ahead = [&](int seg) { // at segment seg, and its first tile's mask
+            if (!wait_warp(sh.d_full[seg & 3], (seg >> 2) & 1))
+                return;
+            d_next = sh.seg[seg & 3];
+            live = tid < d_next.rows;
+            words = p.mask + (size_t)(d_next.row0 + (live ? node : 0)) * p.mask_words;
+            if (live && masked(d_next, d_next.tile0))
+                ahead.load(words, p.mask_words, d_next.tile0 * kTreeTile, d_next.ctx);
+        };
+        look_ahead(0);
+        for (int seg = 0; ok; ++seg) {
+            d = d_next;
+            const bool warp_live = warp * 32 < d.rows, now_live = live;
             float m = -INFINITY, l = 0.f;
             bool saw = false, poison = false;
             for (int tile = d.tile0; tile < d.tile1 && ok; ++tile, ++it) {
                 const uint32_t s_column = tmem + lanes + C::kS0 + (it & 1) * kTreeTile;
                 const int t0 = tile * kTreeTile, st = it % NS;
-                const bool special = t0 + kTreeTile > d.ctx; // uniform over the CTA
+                const bool special = masked(d, tile); // uniform over the CTA
                 uint64_t seen = ~0ull;
                 if (special)
-                    seen = live ? tree_seen(words, p.mask_words, t0, d.ctx, d.n) : 0ull;
+                    seen = live ? ahead.bits(t0, d.ctx, d.n) : 0ull;
                 if (!wait_warp(sh.s_full[it & 1], (it >> 1) & 1))
                     break;
                 tcgen05_fence_after();
@@ -714,22 +816,18 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         break;
                     poison = *(volatile int32_t *)&sh.poison[seg & 3] != 0;
                 }
+                constexpr int kPieces = D / 16;
+                const int vj = tid >> 1; // this thread's row of V, and its pieces
+                const uint32_t v_tile = v_tiles + st * C::kTileBytes;
                 if (special) {
-                    // Two threads a row of V: rows behind the last token
-                    // become zero, rows of nodes are looked through.
-                    const int j = tid >> 1;
-                    const uint32_t v = v_tiles + st * C::kTileBytes;
-                    constexpr int kPieces = D / 16;
+                    // Two threads a row of V: those of nodes, and behind the last
+                    // token, are looked through.
                     bool bad = false;
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         const uint32_t at =
-                            v + tree_piece_at<D>(j, (tid & 1) * kPieces + i);
-                        if (t0 + j >= d.n) {
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at),
-                                         "r"(0)
-                                         : "memory");
-                        } else if (t0 + j >= d.ctx) {
+                            v_tile + tree_piece_at<D>(vj, (tid & 1) * kPieces + i);
+                        if (t0 + vj >= d.ctx) {
                             uint4 x;
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
@@ -739,63 +837,79 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                     }
                     if (bad)
-                        atomicOr(&sh.strange[j >> 5], 1u << (j & 31));
-                    fence_proxy_async_smem();
+                        atomicOr(&sh.strange[vj >> 5], 1u << (vj & 31));
                     if (!sync_warps())
                         break;
                     strange = (uint64_t)*(volatile uint32_t *)&sh.strange[1] << 32 |
                               *(volatile uint32_t *)&sh.strange[0];
                 }
-                uint32_t x[64];
+                constexpr int NC = kTreeTile;
+                uint32_t x[NC];
                 float alpha = 1.f;
                 bool rescale = false;
-                if (warp_live) {
-                    tmem_ld_x64(s_column, x);
-                    float mx[4];
-                    const bool up = c >= 0.f;
-                    if (special) {
+                // Two bodies, so that tiles that every row sees whole carry
+                // none of the masking.
+                const auto softmax = [&](auto is_masked) {
+                    constexpr bool kMasked = decltype(is_masked)::value;
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
+                    for (int k = 0; k < NC; k += 32)
+                        tmem_ld_x32(s_column + k, x + k);
+                    const bool up = c >= 0.f;
+                    if (kMasked) {
+#pragma unroll
+                        for (int k = 0; k < NC; ++k)
                             if (!((seen >> k) & 1))
                                 x[k] = __float_as_uint(up ? -INFINITY : INFINITY);
-                        saw |= seen != 0;
-                    } else {
-                        saw = true;
                     }
+                    saw |= !kMasked || seen != 0;
+                    float mx[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mx[k] = __uint_as_float(x[k]);
                     if (up) {
 #pragma unroll
-                        for (int k = 4; k < 64; ++k)
-                            mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
-                        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        for (int k = 4; k < NC - 4; k += 2)
+                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]),
+                                                    __uint_as_float(x[k + 1]));
+                        mx[0] = max3(mx[0], __uint_as_float(x[NC - 4]), __uint_as_float(x[NC - 3]));
+                        mx[1] = max3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
+                        mx[0] = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                     } else {
 #pragma unroll
-                        for (int k = 4; k < 64; ++k)
-                            mx[k & 3] = fminf(mx[k & 3], __uint_as_float(x[k]));
-                        mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
+                        for (int k = 4; k < NC - 4; k += 2)
+                            mx[(k >> 1) & 3] = min3(mx[(k >> 1) & 3], __uint_as_float(x[k]),
+                                                    __uint_as_float(x[k + 1]));
+                        mx[0] = min3(mx[0], __uint_as_float(x[NC - 4]), __uint_as_float(x[NC - 3]));
+                        mx[1] = min3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
+                        mx[0] = min3(mx[0], mx[1], fminf(mx[2], mx[3]));
                     }
-                    const float top = seen ? mx[0] * c : -INFINITY;
+                    const float top = !kMasked || seen != 0 ? mx[0] * c : -INFINITY;
                     if (top > m + kTreeSlack || (m == -INFINITY && top > m)) {
                         alpha = m == -INFINITY ? 0.f : ex2(m - top);
                         rescale = tile > d.tile0;
                         m = top;
                     }
                     const float off = kTreeBias - (m == -INFINITY ? 0.f : m);
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        float w = ex2(fmaf(__uint_as_float(x[k]), c, off));
-                        if (special && !((seen >> k) & 1))
-                            w = 0.f;
-                        sum[k & 3] += w;
-                        x[k] = __float_as_uint(w);
+                    for (int k = 0; k < NC / 2; ++k) {
+                        float2 w = fma_f32x2(make_float2(__uint_as_float(x[2 * k]),
+                                                         __uint_as_float(x[2 * k + 1])),
+                                             c2, off2);
+                        w.x = ex2(w.x);
+                        w.y = ex2(w.y);
+                        sum[k & 1] = add_f32x2(sum[k & 1], w);
+                        x[k] = pack2<QT>(w.x, w.y); // in place: pair k is done with x[2k..]
                     }
-                    l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        x[k] = pack2<QT>(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+                    sum[0] = add_f32x2(sum[0], sum[1]);
+                    l = fmaf(l, alpha, sum[0].x + sum[0].y);
+                };
+                if (warp_live) {
+                    if (special)
+                        softmax(std::true_type{});
+                    else
+                        softmax(std::false_type{});
                 }
                 // O is complete up to the tile before.
                 if (tile > d.tile0) {
@@ -819,7 +933,6 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                     tmem_wait_st();
                 }
                 if (strange) {
-                    const uint32_t v = v_tiles + st * C::kTileBytes;
                     if (tile == d.tile0) {
                         uint32_t o[32];
 #pragma unroll
@@ -831,16 +944,18 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         if (tid == 0)
                             *(volatile int32_t *)&sh.keep_o = it;
                     }
-                    if (warp_live)
-                        rescue_rows<QT, D>(strange, seen, v, s_column, o_column);
+                    if (warp_live) {
+                        const int nodes = d.n - t0; // rows behind are just emptied
+                        rescue_rows<QT, D>(nodes < 64 ? strange & ((1ull << nodes) - 1) : strange,
+                                           seen, v_tile, s_column, o_column);
+                    }
                     if (!sync_warps())
                         break;
-                    const int j = tid >> 1;
-                    if ((strange >> j) & 1)
-                        for (int i = 0; i < D / 16; ++i)
+                    if ((strange >> vj) & 1)
+                        for (int i = 0; i < kPieces; ++i)
                             asm volatile(
                                 "st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                    v + tree_piece_at<D>(j, (tid & 1) * (D / 16) + i)),
+                                    v_tile + tree_piece_at<D>(vj, (tid & 1) * kPieces + i)),
                                 "r"(0)
                                 : "memory");
                     if (tid < 2)
@@ -853,7 +968,12 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&sh.p_full[it & 1]));
+                if (tile + 1 < d.tile1 && live && masked(d, tile + 1))
+                    ahead.load(words, p.mask_words, t0 + kTreeTile, d.ctx);
             }
+            // Before this segment's rows are written, for the latency.
+            if (ok && !d.last)
+                look_ahead(seg + 1);
             if (!ok || !wait_warp(sh.o_full, (it - 1) & 1))
                 break;
             tcgen05_fence_after();
@@ -863,7 +983,7 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                 const bool none = l == 0.f && !saw;
                 if (d.slot < 0) {
                     const float inv = none ? 0.f : 1.f / l;
-                    const size_t row =
+                    const size_t at =
                         ((size_t)(d.row0 + node) * p.num_heads + d.kv_head * p.group +
                          (tid - node * p.group)) * D;
 #pragma unroll 1
@@ -875,8 +995,8 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                             o[k] = __float_as_uint(poison ? NAN
                                                    : none ? 0.f
                                                           : __uint_as_float(o[k]) * inv);
-                        if (live)
-                            store_row32(p.out, p.out_dtype, row + c0, o);
+                        if (now_live)
+                            store_row32(p.out, p.out_dtype, at + c0, o);
                         __syncwarp();
                     }
                 } else {
@@ -886,7 +1006,7 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t o[32];
                         tmem_ld_x32(o_column + c0, o);
-                        if (live) {
+                        if (now_live) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 __stcg(acc + (size_t)(c0 / 4 + k) * kTreeRows,
@@ -897,7 +1017,7 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         __syncwarp();
                     }
-                    if (live) // l = -0: the row saw only scores of minus infinity
+                    if (now_live) // l = -0: the row saw only scores of minus infinity
                         __stcg(p.ws_ml + slot * kTreeRows + tid,
                                make_float2(m, poison ? NAN : l == 0.f && saw ? -0.f : l));
                 }
@@ -906,13 +1026,15 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(smem_addr(&sh.o_free));
+            if (d.last)
+                break;
         }
     }
     if (!ok)
         report(p.dev_err, PA_DEVERR_TIMEOUT);
     tcgen05_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kSoftmaxWarps + 2) {
         tcgen05_fence_after();
         tmem_dealloc(tmem, C::kColumns);
     }
@@ -920,7 +1042,8 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
 
 // Joins the parts of the unit that is cut before CTA blockIdx.x, if there is
 // one and no earlier cut in it: O = sum_p 2^(m_p - M) acc_p / sum_p
-// 2^(m_p - M) l_p. A thread has one row and D / 4 / gridDim.y columns of four.
+// 2^(m_p - M) l_p. A thread has one row and kMergeCols columns of four.
+constexpr int kMergeCols = 2;
 template <int D>
 __global__ void __launch_bounds__(kTreeRows) tree_merge_kernel(
     const __grid_constant__ TreeDecodeParams p)
@@ -933,35 +1056,52 @@ __global__ void __launch_bounds__(kTreeRows) tree_merge_kernel(
     if (rec.parts == 0 || row >= rec.rows)
         return;
     const auto slot = [&](int i) { return i == 0 ? (size_t)(b - 1) * 2 + 1 : (size_t)(b + i - 1) * 2; };
-    float M = -INFINITY;
-    for (int i = 0; i < rec.parts; ++i)
-        M = fmaxf(M, __ldcg(p.ws_ml + slot(i) * kTreeRows + row).x);
-    const float use = M == -INFINITY ? 0.f : M;
-    constexpr int kCols = 4;
+    constexpr int kCols = kMergeCols, kChunk = 4; // parts whose loads are in flight together
     const int c0 = blockIdx.y * kCols;
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
     bool saw = false;
     float4 o[kCols];
 #pragma unroll
     for (int k = 0; k < kCols; ++k)
         o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = 0; i < rec.parts; ++i) {
-        const float2 ml = __ldcg(p.ws_ml + slot(i) * kTreeRows + row);
-        const float4 *acc = p.ws_acc + (slot(i) * (D / 4) + c0) * kTreeRows + row;
-        float4 a[kCols];
+    for (int i0 = 0; i0 < rec.parts; i0 += kChunk) {
+        float2 ml[kChunk];
+        float4 a[kChunk][kCols];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (i0 + i < rec.parts) {
+                const size_t at = slot(i0 + i);
+                ml[i] = __ldcg(p.ws_ml + at * kTreeRows + row);
+#pragma unroll
+                for (int k = 0; k < kCols; ++k)
+                    a[i][k] = __ldcg(p.ws_acc + (at * (D / 4) + c0 + k) * kTreeRows + row);
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+            top = fmaxf(top, ml[i].x);
+        const float use = top == -INFINITY ? 0.f : top, keep = ex2(M - use);
+        M = top;
+        L *= keep;
 #pragma unroll
         for (int k = 0; k < kCols; ++k)
-            a[k] = __ldcg(acc + (size_t)k * kTreeRows);
-        const float w = ex2(ml.x - use);
-        saw |= ml.y != 0.f || signbit(ml.y);
-        L = fmaf(ml.y, w, L);
+            o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            o[k].x = fmaf(a[k].x, w, o[k].x);
-            o[k].y = fmaf(a[k].y, w, o[k].y);
-            o[k].z = fmaf(a[k].z, w, o[k].z);
-            o[k].w = fmaf(a[k].w, w, o[k].w);
+        for (int i = 0; i < kChunk; ++i) {
+            if (i0 + i >= rec.parts)
+                break;
+            const float w = ex2(ml[i].x - use);
+            saw |= ml[i].y != 0.f || signbit(ml[i].y);
+            L = fmaf(ml[i].y, w, L);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) {
+                o[k].x = fmaf(a[i][k].x, w, o[k].x);
+                o[k].y = fmaf(a[i][k].y, w, o[k].y);
+                o[k].z = fmaf(a[i][k].z, w, o[k].z);
+                o[k].w = fmaf(a[i][k].w, w, o[k].w);
+            }
         }
     }
     const bool none = L == 0.f && !saw;
