@@ -11,7 +11,6 @@
 #include "host.h"
 #include "last_error.h"
 #include "tree_decode.cuh"
-#include "tree_decode_simple.cuh"
 #include "tree_ops.cuh"
 
 using namespace pagedkv;
@@ -35,14 +34,6 @@ pa_status check_mask_words(int32_t mask_words)
         return fail(PA_ERR_INVALID_ARG, "mask_words %d outside [1, %d]", mask_words,
                     PA_TREE_MAX_NODES / 32);
     return PA_OK;
-}
-
-template <typename T, typename QT>
-cudaError_t launch_tree_simple(const TreeSimpleParams &p, int head_dim, cudaStream_t st)
-{
-    const dim3 grid(p.num_tokens, (p.num_heads + 3) / 4);
-    return head_dim == 64 ? launch_pdl(tree_decode_kernel<T, QT, 64>, grid, dim3(128), 0, st, p)
-                          : launch_pdl(tree_decode_kernel<T, QT, 128>, grid, dim3(128), 0, st, p);
 }
 
 int tree_ctas() { return kTreeCtasPerSm * sm_count_of_current_device(); }
@@ -110,11 +101,11 @@ pa_status encode_tree_pool(CUtensorMap *map, const void *pool, const pa_cache_de
     return PA_OK;
 }
 
-template <typename QT, int D, int BS>
+template <typename T, typename QT, int D, int BS>
 pa_status launch_tree(const TreeTmaParams &g, int ctas, cudaStream_t st)
 {
-    using C = TreeCfg<QT, D, BS>;
-    auto kernel = tree_decode_tc_kernel<QT, D, BS>;
+    using C = TreeCfg<T, D, BS>;
+    auto kernel = tree_decode_kernel<T, QT, D, BS>;
     static std::atomic<size_t> smem_set[kMaxDevices];
     cudaError_t e = allow_smem(kernel, C::kSmem, smem_set);
     if (e != cudaSuccess)
@@ -122,29 +113,30 @@ pa_status launch_tree(const TreeTmaParams &g, int ctas, cudaStream_t st)
     e = launch_pdl(kernel, dim3(ctas), dim3(C::kThreads), C::kSmem, st, g);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_decode launch");
-    e = launch_pdl(tree_merge_kernel<D>, dim3(ctas - 1, D / 4 / kMergeCols), dim3(kTreeRows), 0, st, g.p);
+    e = launch_pdl(tree_merge_kernel<D>, dim3(ctas - 1, D / 4 / kMergeCols), dim3(kTreeRows), 0,
+                   st, g.p);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_merge launch");
     return ok();
 }
 
-template <typename QT, int D>
+template <typename T, typename QT, int D>
 pa_status launch_tree_bs(const TreeTmaParams &g, int block_size, int ctas, cudaStream_t st)
 {
     switch (block_size) {
-    case 8: return launch_tree<QT, D, 8>(g, ctas, st);
-    case 16: return launch_tree<QT, D, 16>(g, ctas, st);
-    case 32: return launch_tree<QT, D, 32>(g, ctas, st);
+    case 8: return launch_tree<T, QT, D, 8>(g, ctas, st);
+    case 16: return launch_tree<T, QT, D, 16>(g, ctas, st);
+    case 32: return launch_tree<T, QT, D, 32>(g, ctas, st);
     }
     return fail(PA_ERR_UNSUPPORTED, "block_size %d", block_size);
 }
 
-template <typename QT>
+template <typename T, typename QT>
 pa_status launch_tree_dim(const TreeTmaParams &g, const pa_cache_desc *c, int ctas,
                           cudaStream_t st)
 {
-    return c->head_dim == 64 ? launch_tree_bs<QT, 64>(g, c->block_size, ctas, st)
-                             : launch_tree_bs<QT, 128>(g, c->block_size, ctas, st);
+    return c->head_dim == 64 ? launch_tree_bs<T, QT, 64>(g, c->block_size, ctas, st)
+                             : launch_tree_bs<T, QT, 128>(g, c->block_size, ctas, st);
 }
 
 } // namespace
@@ -238,34 +230,6 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     if (!aligned16(workspace))
         return fail(PA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cache->dtype == PA_FP8_E4M3) {
-        TreeSimpleParams p;
-        p.out = out;
-        p.query = query;
-        p.key_cache = key_cache;
-        p.value_cache = value_cache;
-        p.block_tables = block_tables;
-        p.context_lens = context_lens;
-        p.tree_start = tree_start;
-        p.mask = mask;
-        p.dev_err = dev_err;
-        p.num_seqs = num_seqs;
-        p.num_tokens = num_tokens;
-        p.num_heads = num_heads;
-        p.num_kv_heads = cache->num_kv_heads;
-        p.num_blocks = cache->num_blocks;
-        p.block_size = cache->block_size;
-        p.max_blocks_per_seq = max_blocks_per_seq;
-        p.mask_words = mask_words;
-        p.out_dtype = (int32_t)out_dtype;
-        p.qk_scale_log2 = scale * 1.4426950408889634f;
-        const cudaError_t e = cache->io_dtype == PA_F16
-                                  ? launch_tree_simple<E4M3, __half>(p, cache->head_dim, st)
-                                  : launch_tree_simple<E4M3, __nv_bfloat16>(p, cache->head_dim, st);
-        if (e != cudaSuccess)
-            return cuda_fail(e, "tree_decode launch");
-        return ok();
-    }
     TreeTmaParams g;
     std::memset(&g, 0, sizeof(g));
     TreeDecodeParams &p = g.p;
@@ -273,6 +237,8 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     const TreeWorkspace w = tree_workspace(ctas, cache->head_dim);
     char *ws = static_cast<char *>(workspace);
     p.out = out;
+    p.key_cache = key_cache;
+    p.value_cache = value_cache;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
     p.tree_start = tree_start;
@@ -295,12 +261,17 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     // number makes every finite score as equal as zero would.
     p.qk_scale_log2 = scale == 0.f ? FLT_MIN : scale * 1.4426950408889634f;
     if ((s = encode_tree_query(&g.q, query, num_tokens, num_heads, p.group, cache->head_dim)) !=
-            PA_OK ||
-        (s = encode_tree_pool(&g.k, key_cache, cache)) != PA_OK ||
+        PA_OK)
+        return s;
+    if (cache->dtype == PA_FP8_E4M3)
+        return cache->io_dtype == PA_F16 ? launch_tree_dim<E4M3, __half>(g, cache, ctas, st)
+                                         : launch_tree_dim<E4M3, __nv_bfloat16>(g, cache, ctas, st);
+    if ((s = encode_tree_pool(&g.k, key_cache, cache)) != PA_OK ||
         (s = encode_tree_pool(&g.v, value_cache, cache)) != PA_OK)
         return s;
-    return cache->dtype == PA_F16 ? launch_tree_dim<__half>(g, cache, ctas, st)
-                                  : launch_tree_dim<__nv_bfloat16>(g, cache, ctas, st);
+    return cache->dtype == PA_F16
+               ? launch_tree_dim<__half, __half>(g, cache, ctas, st)
+               : launch_tree_dim<__nv_bfloat16, __nv_bfloat16>(g, cache, ctas, st);
 }
 
 pa_status pa_tree_accept(int32_t *accepted, int32_t *accepted_lens, int64_t *next_token,

@@ -65,6 +65,7 @@ constexpr int kTreeRows = 128;  // rows of a tile: the MMA's M
 constexpr int kTreeTile = 64;   // tokens of a tile
 constexpr int kTreeCtasPerSm = 2;
 constexpr int kSoftmaxWarps = 4;
+constexpr int kRawStages = 2; // fp8 tiles on their way, of K and of V
 #ifndef PA_TREE_UNIT_COST
 #define PA_TREE_UNIT_COST 4
 #endif
@@ -84,6 +85,7 @@ struct TreeMergeRecord {
 
 struct TreeDecodeParams {
     void *out;
+    const void *key_cache, *value_cache; // fp8 caches; others come through their maps
     const int32_t *block_tables, *context_lens, *tree_start, *mask;
     int32_t *dev_err;
     TreeMergeRecord *ws_records; // [CTAs]
@@ -280,15 +282,19 @@ struct TreeSegment {
 };
 
 template <typename T, int D, int BS> struct TreeCfg {
+    static constexpr bool kFp8 = std::is_same<T, E4M3>::value;
     static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = kTreeTile * D * 2;       // a K or V tile
     static constexpr int kQBytes = kTreeRows * D * 2;
     static constexpr int kGroupBytes = 1024 * kHalves;         // 8 rows
-    static constexpr int kStages = D == 128 ? 2 : 4;           // of K and of V
+    static constexpr int kStages = (D == 128 ? 2 : 4) / (kFp8 ? 2 : 1); // of K and of V
     static constexpr int kBlocks = kTreeTile / BS;             // blocks of a tile
-    static constexpr int kBlockBytes = BS * D * 2;
+    // Bytes of a block in memory, and of the ring that fp8 tiles arrive in.
+    static constexpr int kBlockBytes = kFp8 ? BS * D + 4 * BS : BS * D * 2;
+    static constexpr int kRawBytes = kFp8 ? kBlocks * kBlockBytes : 0;
     static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
-    static constexpr int kSmem = 1024 + kQBytes + 2 * kStages * kTileBytes;
+    static constexpr int kSmem =
+        1024 + kQBytes + 2 * kStages * kTileBytes + 2 * kRawStages * kRawBytes;
     static constexpr uint32_t kColumns = 256;
     static constexpr uint32_t kS0 = D; // tensor-memory column of the first S tile
 };
@@ -303,6 +309,10 @@ template <int NS> struct TreeShared {
     TreeSegment seg[4];
     int32_t poison[4];       // segment met a block id outside the pool
     uint32_t strange[2];     // tokens of a tile whose V row holds NaN or infinity
+    // fp8 caches: raw tiles, and the row scales of four tiles.
+    uint64_t raw_full[2][kRawStages], ks_full[4], vs_full[4];
+    float ks[4][kTreeTile], vs[4][kTreeTile];
+    float vmax[4]; // the largest finite V scale of a tile that every row sees
     uint32_t tmem;
     int32_t keep_o;          // tile whose P V adds to O although it is a segment's first
 };
@@ -459,12 +469,19 @@ template <typename QT> __device__ __forceinline__ bool not_finite(const uint4 &x
 
 // The fetching warps: K tiles of the CTA's piece, with each segment's
 // description and query rows, or its V tiles.
-template <typename QT, int D, int BS, bool kIsV>
+//
+// fp8 tiles come as they are (codes and row scales, one bulk copy per block)
+// into a ring of kRawStages, and are widened from there to the swizzled
+// 16-bit tile by the same warp while the next one is on its way. Scores are
+// multiplied by K's scales and weights by V's in the softmax; the scales go
+// to it on their own barriers.
+template <typename T, typename QT, int D, int BS, bool kIsV>
 __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
-                                           TreeShared<TreeCfg<QT, D, BS>::kStages> &sh,
-                                           uint32_t q_tile, uint32_t ring, bool &ok)
+                                           TreeShared<TreeCfg<T, D, BS>::kStages> &sh,
+                                           uint32_t q_tile, uint32_t ring, uint32_t raw_ring,
+                                           bool &ok)
 {
-    using C = TreeCfg<QT, D, BS>;
+    using C = TreeCfg<T, D, BS>;
     constexpr int NS = C::kStages;
     const TreeDecodeParams &p = g.p;
     const int lane = threadIdx.x & 31, per_tile = kTreeRows / p.group;
@@ -479,6 +496,85 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
     TreeSeq q = tree_seq(p, s, BS);
     int64_t unit_begin = sh.plan.unit_begin;
     int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
+    // Widens tile `of` of the CTA, the first `blocks` blocks of which came.
+    const auto widen = [&](int of, int blocks, int left) {
+        if constexpr (C::kFp8) {
+            const int st = of % NS, raw_st = of % kRawStages;
+            if (!wait(sh.raw_full[kIsV][raw_st], (of / kRawStages) & 1))
+                return;
+            const uint32_t raw = raw_ring + raw_st * C::kRawBytes;
+            float *scales = kIsV ? sh.vs[of & 3] : sh.ks[of & 3];
+            const auto publish = [&]() {
+                float top = 0.f;
+#pragma unroll
+                for (int j = lane; j < kTreeTile; j += 32) {
+                    float x;
+                    asm volatile("ld.shared.f32 %0, [%1];"
+                                 : "=f"(x)
+                                 : "r"(raw + (j / BS) * C::kBlockBytes + BS * D + (j % BS) * 4)
+                                 : "memory");
+                    scales[j] = x;
+                    if (j < left && x < INFINITY)
+                        top = fmaxf(top, x);
+                }
+                if (kIsV) {
+                    for (int o = 16; o > 0; o >>= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    if (lane == 0)
+                        sh.vmax[of & 3] = top;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(kIsV ? &sh.vs_full[of & 3] : &sh.ks_full[of & 3]));
+            };
+            // V's scales are wanted before its tile is free; K's with it.
+            if (kIsV)
+                publish();
+            if (of >= NS && !wait(empty[st], ((of / NS) & 1) ^ 1))
+                return;
+            if (!kIsV)
+                publish();
+            constexpr int kChunks = D / 16; // of 16 codes, per row
+            const uint32_t to = ring + st * C::kTileBytes;
+#pragma unroll 4
+            for (int k = lane; k < kTreeTile * kChunks; k += 32) {
+                const int j = k / kChunks, i = k % kChunks;
+                if (j >= blocks * BS)
+                    break;
+                uint4 code;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(code.x), "=r"(code.y), "=r"(code.z), "=r"(code.w)
+                             : "r"(raw + (j / BS) * C::kBlockBytes + (j % BS) * D + i * 16)
+                             : "memory");
+                uint32_t w[8];
+                Store<E4M3>::to_h2(code, w);
+                if (std::is_same<QT, __nv_bfloat16>::value) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float2 f = h2_to_float2(w[e]);
+                        w[e] = pack2<__nv_bfloat16>(f.x, f.y);
+                    }
+                }
+                // Lanes of a row's second half store their pieces in the
+                // other order: 8 lanes then meet 8 different bank groups.
+                const int turn = i >= 4 ? 1 : 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int piece = u ^ turn;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     to + tree_piece_at<D>(j, 2 * i + piece)),
+                                 "r"(piece ? w[4] : w[0]), "r"(piece ? w[5] : w[1]),
+                                 "r"(piece ? w[6] : w[2]), "r"(piece ? w[7] : w[3])
+                                 : "memory");
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&full[st]));
+        }
+    };
+    int to_widen = 0, to_widen_left = 0; // blocks and tokens of the tile before
     uint32_t q_seen[2] = {0, 0}; // segments of each parity whose query rows were seen done
     bool was_whole = false;
     for (bool last = false; !last && ok; ++seg) {
@@ -499,13 +595,16 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
             const int left = n - tile * kTreeTile; // tokens from here on
             const int blocks = left <= 0 ? 0 : min(C::kBlocks, (left + BS - 1) / BS);
             const int next = tile + 1 < end ? block_id(tile + 1) : -1;
-            if (it >= NS && !wait(empty[st], ph ^ 1))
+            if (!C::kFp8 && it >= NS && !wait(empty[st], ph ^ 1))
                 break;
             // Only now, so that the table's latency passes during the wait.
             const bool bad = lane < blocks && (id < 0 || id >= p.num_blocks);
             const bool any_bad = __any_sync(0xffffffffu, bad);
-            const int row8 = (int)((((int64_t)(bad ? 0 : id) * p.num_kv_heads + h) * BS) >> 3);
-            const uint32_t bar = smem_addr(&full[st]), to = ring + st * C::kTileBytes;
+            const int64_t tile_at = (int64_t)(bad ? 0 : id) * p.num_kv_heads + h;
+            const uint32_t bar = smem_addr(C::kFp8 ? &sh.raw_full[kIsV][it % kRawStages]
+                                                   : &full[st]);
+            const uint32_t to = C::kFp8 ? raw_ring + (it % kRawStages) * C::kRawBytes
+                                        : ring + st * C::kTileBytes;
             if (elect_one()) {
                 if (kIsV && tile == tile0)
                     sh.poison[seg & 3] = q.bad_context;
@@ -519,10 +618,26 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
             __syncwarp();
 #pragma unroll
             for (int b = 0; b < C::kBlocks; ++b) {
-                const int y = __shfl_sync(0xffffffffu, row8, b);
-                if (b < blocks && elect_one())
-                    tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, y, bar);
+                const int64_t at = __shfl_sync(0xffffffffu, tile_at, b);
+                if (b < blocks && elect_one()) {
+                    if constexpr (C::kFp8)
+                        bulk_g2s(to + b * C::kBlockBytes,
+                                 static_cast<const uint8_t *>(kIsV ? p.value_cache : p.key_cache) +
+                                     at * C::kBlockBytes,
+                                 C::kBlockBytes, bar);
+                    else
+                        tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, (int)(at * BS >> 3),
+                                    bar);
+                }
                 __syncwarp();
+            }
+            if constexpr (C::kFp8) {
+                if (it > 0)
+                    widen(it - 1, to_widen, to_widen_left);
+                if (!ok)
+                    break;
+                to_widen = blocks;
+                to_widen_left = left;
             }
             if (!kIsV && tile == tile0) {
                 // A segment of up to 64 rows takes half of the query area,
@@ -581,20 +696,25 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
             q = tree_seq(p, s, BS);
         }
     }
+    if (C::kFp8 && ok)
+        widen(it - 1, to_widen, to_widen_left);
     if (!ok) { // let the copies in flight land before the CTA goes
         constexpr uint64_t kDrainNs = 10000000;
-        for (int i = max(0, it - NS + 1); i <= it; ++i)
-            mbar_wait_bounded(smem_addr(&full[i % NS]), (i / NS) & 1, kDrainNs);
+        constexpr int kRing = C::kFp8 ? kRawStages : NS;
+        for (int i = max(0, it - kRing + 1); i <= it; ++i)
+            mbar_wait_bounded(smem_addr(C::kFp8 ? &sh.raw_full[kIsV][i % kRing] : &full[i % kRing]),
+                              (i / kRing) & 1, kDrainNs);
         if (!kIsV)
             mbar_wait_bounded(smem_addr(&sh.q_full[seg & 3]), (seg >> 2) & 1, kDrainNs);
     }
 }
 
-template <typename QT, int D, int BS>
-__global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
-    tree_decode_tc_kernel(const __grid_constant__ TreeTmaParams g)
+// T: the cache's storage, QT: the type of query rows and of the products.
+template <typename T, typename QT, int D, int BS>
+__global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
+    tree_decode_kernel(const __grid_constant__ TreeTmaParams g)
 {
-    using C = TreeCfg<QT, D, BS>;
+    using C = TreeCfg<T, D, BS>;
     constexpr int NS = C::kStages;
     constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
     extern __shared__ __align__(1024) uint8_t tree_dyn[];
@@ -603,7 +723,8 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_addr(tree_dyn) + 1023u) & ~1023u;
     const uint32_t q_tile = base, k_tiles = base + C::kQBytes,
-                   v_tiles = k_tiles + NS * C::kTileBytes;
+                   v_tiles = k_tiles + NS * C::kTileBytes,
+                   raw_tiles = v_tiles + NS * C::kTileBytes;
 
     pdl_launch_dependents();
     if (tid == 0) {
@@ -615,10 +736,14 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(smem_addr(&sh.d_full[i]), 1);
+            mbar_init(smem_addr(&sh.ks_full[i]), 1);
+            mbar_init(smem_addr(&sh.vs_full[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.q_empty[i]), 1);
+            for (int k = 0; k < kRawStages; ++k)
+                mbar_init(smem_addr(&sh.raw_full[i][k]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.p_full[i]), kSoftmaxWarps);
         }
@@ -647,9 +772,10 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
         if (tid == 0)
             p.ws_records[blockIdx.x].parts = 0;
     } else if (warp == kSoftmaxWarps) {
-        tree_fetch<QT, D, BS, false>(g, sh, q_tile, k_tiles, ok);
+        tree_fetch<T, QT, D, BS, false>(g, sh, q_tile, k_tiles, raw_tiles, ok);
     } else if (warp == kSoftmaxWarps + 1) {
-        tree_fetch<QT, D, BS, true>(g, sh, q_tile, v_tiles, ok);
+        tree_fetch<T, QT, D, BS, true>(g, sh, q_tile, v_tiles,
+                                       raw_tiles + kRawStages * C::kRawBytes, ok);
     } else if (warp == kSoftmaxWarps + 2) {
         // --- MMAs: the warp waits together, one lane issues ---------------------------------
         constexpr uint32_t kIdescQk = umma_idesc(kBf16, false, kTreeRows, kTreeTile);
@@ -797,6 +923,7 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
             d = d_next;
             const bool warp_live = warp * 32 < d.rows, now_live = live;
             float m = -INFINITY, l = 0.f;
+            float R = 0.f; // fp8: a power of two, O is in units of
             bool saw = false, poison = false;
             for (int tile = d.tile0; tile < d.tile1 && ok; ++tile, ++it) {
                 const uint32_t s_column = tmem + lanes + C::kS0 + (it & 1) * kTreeTile;
@@ -845,8 +972,11 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                 }
                 constexpr int NC = kTreeTile;
                 uint32_t x[NC];
-                float alpha = 1.f;
+                float alpha = 1.f, keep = 1.f; // what O, and l, are multiplied by
                 bool rescale = false;
+                if (C::kFp8 && (!wait_warp(sh.ks_full[it & 3], (it >> 2) & 1) ||
+                                !wait_warp(sh.vs_full[it & 3], (it >> 2) & 1)))
+                    break;
                 // Two bodies, so that tiles that every row sees whole carry
                 // none of the masking.
                 const auto softmax = [&](auto is_masked) {
@@ -854,7 +984,49 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
 #pragma unroll
                     for (int k = 0; k < NC; k += 32)
                         tmem_ld_x32(s_column + k, x + k);
-                    const bool up = c >= 0.f;
+                    float factor = c;
+                    [[maybe_unused]] float inv_R = 0.f;
+                    if constexpr (C::kFp8) {
+                        const float4 *ks = reinterpret_cast<const float4 *>(sh.ks[it & 3]);
+#pragma unroll
+                        for (int k = 0; k < NC / 4; ++k) {
+                            const float4 s4 = ks[k];
+                            const float f[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const float2 y = mul_f32x2(
+                                    make_float2(__uint_as_float(x[4 * k + e]),
+                                                __uint_as_float(x[4 * k + e + 1])),
+                                    mul_f32x2(make_float2(f[e], f[e + 1]), make_float2(c, c)));
+                                x[4 * k + e] = __float_as_uint(y.x);
+                                x[4 * k + e + 1] = __float_as_uint(y.y);
+                            }
+                        }
+                        factor = 1.f;
+                        // V's scales relative to R, the power of two above
+                        // the largest so far: p * scale / R stays in f16's
+                        // range whatever the scales.
+                        float top_v = sh.vmax[it & 3];
+                        if (kMasked) {
+                            top_v = 0.f;
+#pragma unroll
+                            for (int k = 0; k < NC; ++k) {
+                                const float v = sh.vs[it & 3][k];
+                                if (((seen >> k) & 1) && v < INFINITY)
+                                    top_v = fmaxf(top_v, v);
+                            }
+                        }
+                        if (top_v > R) {
+                            const float up2 = __uint_as_float(
+                                min((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u,
+                                    0x7e800000u));
+                            alpha = R / up2;
+                            rescale = tile > d.tile0;
+                            R = up2;
+                        }
+                        inv_R = R > 0.f ? 1.f / R : 0.f;
+                    }
+                    const bool up = C::kFp8 || c >= 0.f;
                     if (kMasked) {
 #pragma unroll
                         for (int k = 0; k < NC; ++k)
@@ -883,14 +1055,15 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         mx[1] = min3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
                         mx[0] = min3(mx[0], mx[1], fminf(mx[2], mx[3]));
                     }
-                    const float top = !kMasked || seen != 0 ? mx[0] * c : -INFINITY;
+                    const float top = !kMasked || seen != 0 ? mx[0] * factor : -INFINITY;
                     if (top > m + kTreeSlack || (m == -INFINITY && top > m)) {
-                        alpha = m == -INFINITY ? 0.f : ex2(m - top);
+                        keep = m == -INFINITY ? 0.f : ex2(m - top);
+                        alpha *= keep;
                         rescale = tile > d.tile0;
                         m = top;
                     }
                     const float off = kTreeBias - (m == -INFINITY ? 0.f : m);
-                    const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+                    const float2 c2 = make_float2(factor, factor), off2 = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int k = 0; k < NC / 2; ++k) {
@@ -900,10 +1073,18 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         w.x = ex2(w.x);
                         w.y = ex2(w.y);
                         sum[k & 1] = add_f32x2(sum[k & 1], w);
+                        if constexpr (C::kFp8) {
+                            float2 v = *reinterpret_cast<const float2 *>(&sh.vs[it & 3][2 * k]);
+                            if (kMasked) { // what is not seen may be NaN
+                                v.x = (seen >> (2 * k)) & 1 ? v.x : 0.f;
+                                v.y = (seen >> (2 * k + 1)) & 1 ? v.y : 0.f;
+                            }
+                            w = mul_f32x2(w, mul_f32x2(v, make_float2(inv_R, inv_R)));
+                        }
                         x[k] = pack2<QT>(w.x, w.y); // in place: pair k is done with x[2k..]
                     }
                     sum[0] = add_f32x2(sum[0], sum[1]);
-                    l = fmaf(l, alpha, sum[0].x + sum[0].y);
+                    l = fmaf(l, keep, sum[0].x + sum[0].y);
                 };
                 if (warp_live) {
                     if (special)
@@ -982,7 +1163,7 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                 // minus infinity is NaN, as 0/0 is.
                 const bool none = l == 0.f && !saw;
                 if (d.slot < 0) {
-                    const float inv = none ? 0.f : 1.f / l;
+                    const float inv = none ? 0.f : C::kFp8 ? R / l : 1.f / l;
                     const size_t at =
                         ((size_t)(d.row0 + node) * p.num_heads + d.kv_head * p.group +
                          (tid - node * p.group)) * D;
@@ -1007,6 +1188,11 @@ __global__ void __launch_bounds__(TreeCfg<QT, D, BS>::kThreads, kTreeCtasPerSm)
                         uint32_t o[32];
                         tmem_ld_x32(o_column + c0, o);
                         if (now_live) {
+                            if constexpr (C::kFp8) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * R);
+                            }
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 __stcg(acc + (size_t)(c0 / 4 + k) * kTreeRows,
