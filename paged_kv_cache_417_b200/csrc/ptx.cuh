@@ -240,13 +240,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-__device__ __forceinline__ float min3(float a, float b, float c)
-{
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // --- tcgen05: tensor-memory allocation, MMAs and moves ---------------------------------------
 
 // A whole warp allocates `columns` (a power of two >= 32) of tensor memory
@@ -367,6 +360,9 @@ __device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint3
     return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) |
            ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
+
+// A's sign in an instruction descriptor.
+constexpr uint32_t kUmmaNegateA = 1u << 13;
 
 // Instruction descriptor of kind::f16 with fp32 accumulators: both operands
 // f16 or both bf16, A K-major, B K-major or MN-major.

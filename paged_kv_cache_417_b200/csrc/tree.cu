@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <cmath>
 #include <cstring>
 
 #include "pagedkv.h"
@@ -259,7 +260,8 @@ pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32
     p.q_box_rows = tree_box_rows(p.group);
     // Never zero: a masked score is -infinity times this. The smallest normal
     // number makes every finite score as equal as zero would.
-    p.qk_scale_log2 = scale == 0.f ? FLT_MIN : scale * 1.4426950408889634f;
+    p.negate = scale < 0.f;
+    p.qk_scale_log2 = scale == 0.f ? FLT_MIN : std::fabs(scale) * 1.4426950408889634f;
     if ((s = encode_tree_query(&g.q, query, num_tokens, num_heads, p.group, cache->head_dim)) !=
         PA_OK)
         return s;

@@ -36,7 +36,7 @@
 //
 // Masks. A tile that ends before the context does is seen by every row. Tiles
 // at and behind the context's end take the slower path: scores that a row
-// does not see become minus infinity (plus, for a negative scale). A product
+// does not see become minus infinity. A product
 // 0 * NaN would still reach a row, so in those tiles the V rows of nodes and
 // behind the last token are looked through, and one that holds a NaN or an
 // infinity is zeroed in shared memory and, if it is a node's, added to the
@@ -94,7 +94,8 @@ struct TreeDecodeParams {
     int32_t num_seqs, num_tokens, num_heads, num_kv_heads, group, num_blocks;
     int32_t max_blocks_per_seq, mask_words, out_dtype;
     int32_t q_box_rows; // rows of a query box: 64 where the group divides it
-    float qk_scale_log2;
+    int32_t negate;     // multiply by -Q K^T ...
+    float qk_scale_log2; // ... and by this, above zero
 };
 
 struct TreeTmaParams {
@@ -468,15 +469,16 @@ template <typename QT> __device__ __forceinline__ bool not_finite(const uint4 &x
 }
 
 // The fetching warps: K tiles of the CTA's piece, with each segment's
-// description and query rows, or its V tiles.
+// description and query rows, or its V tiles. One body for both: the roles of
+// this kernel run at once and share the instruction cache.
 //
 // fp8 tiles come as they are (codes and row scales, one bulk copy per block)
 // into a ring of kRawStages, and are widened from there to the swizzled
 // 16-bit tile by the same warp while the next one is on its way. Scores are
 // multiplied by K's scales and weights by V's in the softmax; the scales go
 // to it on their own barriers.
-template <typename T, typename QT, int D, int BS, bool kIsV>
-__device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
+template <typename T, typename QT, int D, int BS>
+__device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is_v,
                                            TreeShared<TreeCfg<T, D, BS>::kStages> &sh,
                                            uint32_t q_tile, uint32_t ring, uint32_t raw_ring,
                                            bool &ok)
@@ -490,8 +492,9 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
                         ok && mbar_wait_suspended(smem_addr(&bar), parity, kWaitLimitNs));
         return ok;
     };
-    uint64_t *full = kIsV ? sh.v_full : sh.k_full, *empty = kIsV ? sh.v_empty : sh.k_empty;
-    const CUtensorMap *map = kIsV ? &g.v : &g.k;
+    uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
+    const CUtensorMap *map = is_v ? &g.v : &g.k;
+    const uint8_t *pool = static_cast<const uint8_t *>(is_v ? p.value_cache : p.key_cache);
     int s = sh.plan.seq;
     TreeSeq q = tree_seq(p, s, BS);
     int64_t unit_begin = sh.plan.unit_begin;
@@ -500,10 +503,10 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
     const auto widen = [&](int of, int blocks, int left) {
         if constexpr (C::kFp8) {
             const int st = of % NS, raw_st = of % kRawStages;
-            if (!wait(sh.raw_full[kIsV][raw_st], (of / kRawStages) & 1))
+            if (!wait(sh.raw_full[is_v][raw_st], (of / kRawStages) & 1))
                 return;
             const uint32_t raw = raw_ring + raw_st * C::kRawBytes;
-            float *scales = kIsV ? sh.vs[of & 3] : sh.ks[of & 3];
+            float *scales = is_v ? sh.vs[of & 3] : sh.ks[of & 3];
             const auto publish = [&]() {
                 float top = 0.f;
 #pragma unroll
@@ -517,7 +520,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
                     if (j < left && x < INFINITY)
                         top = fmaxf(top, x);
                 }
-                if (kIsV) {
+                if (is_v) {
                     for (int o = 16; o > 0; o >>= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     if (lane == 0)
@@ -525,47 +528,56 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
                 }
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(kIsV ? &sh.vs_full[of & 3] : &sh.ks_full[of & 3]));
+                    mbar_arrive(smem_addr(is_v ? &sh.vs_full[of & 3] : &sh.ks_full[of & 3]));
             };
             // V's scales are wanted before its tile is free; K's with it.
-            if (kIsV)
+            if (is_v)
                 publish();
             if (of >= NS && !wait(empty[st], ((of / NS) & 1) ^ 1))
                 return;
-            if (!kIsV)
+            if (!is_v)
                 publish();
-            constexpr int kChunks = D / 16; // of 16 codes, per row
-            const uint32_t to = ring + st * C::kTileBytes;
-#pragma unroll 4
-            for (int k = lane; k < kTreeTile * kChunks; k += 32) {
-                const int j = k / kChunks, i = k % kChunks;
-                if (j >= blocks * BS)
-                    break;
-                uint4 code;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(code.x), "=r"(code.y), "=r"(code.z), "=r"(code.w)
-                             : "r"(raw + (j / BS) * C::kBlockBytes + (j % BS) * D + i * 16)
-                             : "memory");
-                uint32_t w[8];
-                Store<E4M3>::to_h2(code, w);
-                if (std::is_same<QT, __nv_bfloat16>::value) {
+            // A step takes 32 chunks of 16 codes: kRows rows, a chunk a lane.
+            constexpr int kChunks = D / 16, kRows = 32 / kChunks;
+            const int i = lane % kChunks, r0 = lane / kChunks;
+            // Lanes of a row's second half store their two pieces in the
+            // other order: 8 lanes then meet 8 different bank groups.
+            const bool turn = i >= 4;
+            uint32_t at[8 / kRows][2]; // in a group of 8 rows, for each of its steps
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 f = h2_to_float2(w[e]);
-                        w[e] = pack2<__nv_bfloat16>(f.x, f.y);
-                    }
-                }
-                // Lanes of a row's second half store their pieces in the
-                // other order: 8 lanes then meet 8 different bank groups.
-                const int turn = i >= 4 ? 1 : 0;
+            for (int q = 0; q < 8 / kRows; ++q)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int piece = u ^ turn;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     to + tree_piece_at<D>(j, 2 * i + piece)),
-                                 "r"(piece ? w[4] : w[0]), "r"(piece ? w[5] : w[1]),
-                                 "r"(piece ? w[6] : w[2]), "r"(piece ? w[7] : w[3])
+                for (int u = 0; u < 2; ++u)
+                    at[q][u] = ring + st * C::kTileBytes +
+                               tree_piece_at<D>(q * kRows + r0, 2 * i + (turn ? 1 - u : u));
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b) {
+                const uint32_t from = raw + b * C::kBlockBytes + lane * 16;
+#pragma unroll
+                for (int r = 0; r < BS; r += kRows) {
+                    uint4 code;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(code.x), "=r"(code.y), "=r"(code.z), "=r"(code.w)
+                                 : "r"(from + r * D)
                                  : "memory");
+                    uint32_t w[8];
+                    Store<E4M3>::to_h2(turn ? make_uint4(code.z, code.w, code.x, code.y) : code,
+                                       w);
+                    if (std::is_same<QT, __nv_bfloat16>::value) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 f = h2_to_float2(w[e]);
+                            w[e] = pack2<__nv_bfloat16>(f.x, f.y);
+                        }
+                    }
+                    const uint32_t group = (b * BS + r) / 8 * C::kGroupBytes;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         at[r % 8 / kRows][u] + group),
+                                     "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]),
+                                     "r"(w[4 * u + 3])
+                                     : "memory");
                 }
             }
             fence_proxy_async_smem();
@@ -600,37 +612,37 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
             // Only now, so that the table's latency passes during the wait.
             const bool bad = lane < blocks && (id < 0 || id >= p.num_blocks);
             const bool any_bad = __any_sync(0xffffffffu, bad);
-            const int64_t tile_at = (int64_t)(bad ? 0 : id) * p.num_kv_heads + h;
-            const uint32_t bar = smem_addr(C::kFp8 ? &sh.raw_full[kIsV][it % kRawStages]
+            const int tile_at = (bad ? 0 : id) * p.num_kv_heads + h; // (block, head) tile
+            const uint32_t bar = smem_addr(C::kFp8 ? &sh.raw_full[is_v][it % kRawStages]
                                                    : &full[st]);
             const uint32_t to = C::kFp8 ? raw_ring + (it % kRawStages) * C::kRawBytes
                                         : ring + st * C::kTileBytes;
+            int from[C::kBlocks];
+#pragma unroll
+            for (int b = 0; b < C::kBlocks; ++b)
+                from[b] = __shfl_sync(0xffffffffu, tile_at, b);
             if (elect_one()) {
-                if (kIsV && tile == tile0)
+                if (is_v && tile == tile0)
                     sh.poison[seg & 3] = q.bad_context;
                 if (any_bad) {
                     report(p.dev_err, PA_DEVERR_BLOCK_ID);
-                    if (kIsV)
+                    if (is_v)
                         sh.poison[seg & 3] = 1;
                 }
                 mbar_arrive_expect_tx(bar, blocks * C::kBlockBytes);
-            }
-            __syncwarp();
 #pragma unroll
-            for (int b = 0; b < C::kBlocks; ++b) {
-                const int64_t at = __shfl_sync(0xffffffffu, tile_at, b);
-                if (b < blocks && elect_one()) {
+                for (int b = 0; b < C::kBlocks; ++b) {
+                    if (b >= blocks)
+                        break;
                     if constexpr (C::kFp8)
                         bulk_g2s(to + b * C::kBlockBytes,
-                                 static_cast<const uint8_t *>(kIsV ? p.value_cache : p.key_cache) +
-                                     at * C::kBlockBytes,
-                                 C::kBlockBytes, bar);
+                                 pool + (int64_t)from[b] * C::kBlockBytes, C::kBlockBytes, bar);
                     else
-                        tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, (int)(at * BS >> 3),
+                        tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, from[b] * (BS / 8),
                                     bar);
                 }
-                __syncwarp();
             }
+            __syncwarp();
             if constexpr (C::kFp8) {
                 if (it > 0)
                     widen(it - 1, to_widen, to_widen_left);
@@ -639,7 +651,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
                 to_widen = blocks;
                 to_widen_left = left;
             }
-            if (!kIsV && tile == tile0) {
+            if (!is_v && tile == tile0) {
                 // A segment of up to 64 rows takes half of the query area,
                 // so that its rows can come while the last segment's are
                 // still multiplied; a larger one takes all of it.
@@ -702,9 +714,9 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g,
         constexpr uint64_t kDrainNs = 10000000;
         constexpr int kRing = C::kFp8 ? kRawStages : NS;
         for (int i = max(0, it - kRing + 1); i <= it; ++i)
-            mbar_wait_bounded(smem_addr(C::kFp8 ? &sh.raw_full[kIsV][i % kRing] : &full[i % kRing]),
+            mbar_wait_bounded(smem_addr(C::kFp8 ? &sh.raw_full[is_v][i % kRing] : &full[i % kRing]),
                               (i / kRing) & 1, kDrainNs);
-        if (!kIsV)
+        if (!is_v)
             mbar_wait_bounded(smem_addr(&sh.q_full[seg & 3]), (seg >> 2) & 1, kDrainNs);
     }
 }
@@ -771,14 +783,14 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
     if (sh.plan.empty) {
         if (tid == 0)
             p.ws_records[blockIdx.x].parts = 0;
-    } else if (warp == kSoftmaxWarps) {
-        tree_fetch<T, QT, D, BS, false>(g, sh, q_tile, k_tiles, raw_tiles, ok);
-    } else if (warp == kSoftmaxWarps + 1) {
-        tree_fetch<T, QT, D, BS, true>(g, sh, q_tile, v_tiles,
-                                       raw_tiles + kRawStages * C::kRawBytes, ok);
+    } else if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 1) {
+        const bool is_v = warp != kSoftmaxWarps;
+        tree_fetch<T, QT, D, BS>(g, is_v, sh, q_tile, is_v ? v_tiles : k_tiles,
+                                 raw_tiles + (is_v ? kRawStages * C::kRawBytes : 0), ok);
     } else if (warp == kSoftmaxWarps + 2) {
         // --- MMAs: the warp waits together, one lane issues ---------------------------------
-        constexpr uint32_t kIdescQk = umma_idesc(kBf16, false, kTreeRows, kTreeTile);
+        const uint32_t idesc_qk =
+            umma_idesc(kBf16, false, kTreeRows, kTreeTile) | (p.negate ? kUmmaNegateA : 0);
         constexpr uint32_t kIdescPv = umma_idesc(kBf16, true, kTreeRows, D);
         const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, wait(bar, parity));
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tcgen05_mma_ss(s_tile, q0 + (((k / 4) * (kTreeRows * 128) + (k % 4) * 32) >> 4),
-                                   k0 + (((k / 4) * 1024 + (k % 4) * 32) >> 4), kIdescQk, k > 0);
+                                   k0 + (((k / 4) * 1024 + (k % 4) * 32) >> 4), idesc_qk, k > 0);
                 tcgen05_commit(smem_addr(&sh.s_full[it & 1]));
                 tcgen05_commit(smem_addr(&sh.k_empty[st]));
                 if (it + 1 == seg_end)
@@ -1009,7 +1021,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         float top_v = sh.vmax[it & 3];
                         if (kMasked) {
                             top_v = 0.f;
-#pragma unroll
+#pragma unroll 1
                             for (int k = 0; k < NC; ++k) {
                                 const float v = sh.vs[it & 3][k];
                                 if (((seen >> k) & 1) && v < INFINITY)
@@ -1026,35 +1038,24 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         inv_R = R > 0.f ? 1.f / R : 0.f;
                     }
-                    const bool up = C::kFp8 || c >= 0.f;
                     if (kMasked) {
 #pragma unroll
                         for (int k = 0; k < NC; ++k)
                             if (!((seen >> k) & 1))
-                                x[k] = __float_as_uint(up ? -INFINITY : INFINITY);
+                                x[k] = __float_as_uint(-INFINITY);
                     }
                     saw |= !kMasked || seen != 0;
                     float mx[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mx[k] = __uint_as_float(x[k]);
-                    if (up) {
 #pragma unroll
-                        for (int k = 4; k < NC - 4; k += 2)
-                            mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]),
-                                                    __uint_as_float(x[k + 1]));
-                        mx[0] = max3(mx[0], __uint_as_float(x[NC - 4]), __uint_as_float(x[NC - 3]));
-                        mx[1] = max3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
-                        mx[0] = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    } else {
-#pragma unroll
-                        for (int k = 4; k < NC - 4; k += 2)
-                            mx[(k >> 1) & 3] = min3(mx[(k >> 1) & 3], __uint_as_float(x[k]),
-                                                    __uint_as_float(x[k + 1]));
-                        mx[0] = min3(mx[0], __uint_as_float(x[NC - 4]), __uint_as_float(x[NC - 3]));
-                        mx[1] = min3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
-                        mx[0] = min3(mx[0], mx[1], fminf(mx[2], mx[3]));
-                    }
+                    for (int k = 4; k < NC - 4; k += 2)
+                        mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]),
+                                                __uint_as_float(x[k + 1]));
+                    mx[0] = max3(mx[0], __uint_as_float(x[NC - 4]), __uint_as_float(x[NC - 3]));
+                    mx[1] = max3(mx[1], __uint_as_float(x[NC - 2]), __uint_as_float(x[NC - 1]));
+                    mx[0] = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
                     const float top = !kMasked || seen != 0 ? mx[0] * factor : -INFINITY;
                     if (top > m + kTreeSlack || (m == -INFINITY && top > m)) {
                         keep = m == -INFINITY ? 0.f : ex2(m - top);
