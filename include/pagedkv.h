@@ -370,8 +370,9 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
  * Nothing about the lengths is needed on the host: the work is divided on
  * the device, so a captured call can be replayed with other lengths.
  * Precision: products and sums, the softmax and the P.V sums are fp32, the
- * weight p of the P.V products is rounded to the row type (fp8 caches: the
- * io_dtype) first, and the output once, to out_dtype. A block id outside the
+ * weight p of the P.V products is rounded first, to the row type (fp8 caches:
+ * p times the row's V scale over a power of two, to f16), and the output once,
+ * to out_dtype. A block id outside the
  * pool sets PA_DEVERR_BLOCK_ID and makes that sequence's output NaN.
  */
 pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,

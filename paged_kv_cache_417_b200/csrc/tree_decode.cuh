@@ -17,11 +17,14 @@
 //
 // Roles of a CTA's warps:
 //   0-3  one thread per row: softmax, and the rescaling and writing of rows
-//   4, 5 fetch Q and K, and V, by TMA, block by block through the block table
-//        (one warp for both took 1.5k of the 2.6k cycles of a tile to issue
-//        its copies, and held K of the next tile back behind V of this one)
-//   6    issues the MMAs: S = Q K^T (128 x 64, both operands in shared
+//   4    issues the MMAs: S = Q K^T (128 x 64, both operands in shared
 //        memory) and O += P V (128 x D, P in tensor memory)
+//   6, 7 fetch Q and K, and V, by TMA, block by block through the block table
+//        (one warp for both took 1.5k of the 2.6k cycles of a tile to issue
+//        its copies, and held K of the next tile back behind V of this one).
+//        They share their schedulers with the softmax warps of the last 64
+//        rows, which small trees leave idle; warp 5 is only there to put them
+//        where they are.
 // Tensor memory (256 columns a CTA): O in D fp32 columns and two S tiles of
 // 64; P, 16 bits, overwrites the S tile it comes from. S of the next tile is
 // multiplied before P V of this one, so the tensor core works while the
@@ -64,7 +67,7 @@ namespace pagedkv {
 constexpr int kTreeRows = 128;  // rows of a tile: the MMA's M
 constexpr int kTreeTile = 64;   // tokens of a tile
 constexpr int kTreeCtasPerSm = 2;
-constexpr int kSoftmaxWarps = 4;
+constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kFetchKWarp = 6, kFetchVWarp = 7, kTreeWarps = 8;
 constexpr int kRawStages = 2; // fp8 tiles on their way, of K and of V
 #ifndef PA_TREE_UNIT_COST
 #define PA_TREE_UNIT_COST 4
@@ -284,6 +287,9 @@ struct TreeSegment {
 
 template <typename T, int D, int BS> struct TreeCfg {
     static constexpr bool kFp8 = std::is_same<T, E4M3>::value;
+    // The type of P V: e4m3 codes and weights go into f16 better than into
+    // bf16; K takes the query rows' type.
+    using PT = std::conditional_t<kFp8, __half, T>;
     static constexpr int kHalves = D / 64;
     static constexpr int kTileBytes = kTreeTile * D * 2;       // a K or V tile
     static constexpr int kQBytes = kTreeRows * D * 2;
@@ -293,7 +299,7 @@ template <typename T, int D, int BS> struct TreeCfg {
     // Bytes of a block in memory, and of the ring that fp8 tiles arrive in.
     static constexpr int kBlockBytes = kFp8 ? BS * D + 4 * BS : BS * D * 2;
     static constexpr int kRawBytes = kFp8 ? kBlocks * kBlockBytes : 0;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + 3);
+    static constexpr int kThreads = 32 * kTreeWarps;
     static constexpr int kSmem =
         1024 + kQBytes + 2 * kStages * kTileBytes + 2 * kRawStages * kRawBytes;
     static constexpr uint32_t kColumns = 256;
@@ -312,7 +318,8 @@ template <int NS> struct TreeShared {
     uint32_t strange[2];     // tokens of a tile whose V row holds NaN or infinity
     // fp8 caches: raw tiles, and the row scales of four tiles.
     uint64_t raw_full[2][kRawStages], ks_full[4], vs_full[4];
-    float ks[4][kTreeTile], vs[4][kTreeTile];
+    alignas(16) float ks[4][kTreeTile]; // times scale * log2(e)
+    alignas(16) float vs[4][kTreeTile];
     float vmax[4]; // the largest finite V scale of a tile that every row sees
     uint32_t tmem;
     int32_t keep_o;          // tile whose P V adds to O although it is a segment's first
@@ -507,18 +514,29 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                 return;
             const uint32_t raw = raw_ring + raw_st * C::kRawBytes;
             float *scales = is_v ? sh.vs[of & 3] : sh.ks[of & 3];
+            // Rows of V whose scale is no finite number come in full (inf and
+            // NaN are 16-bit values too) with a scale of one, rows behind the
+            // last token with zero: weights of zero then stay zero.
+            uint32_t odd[2] = {0, 0};
             const auto publish = [&]() {
                 float top = 0.f;
 #pragma unroll
-                for (int j = lane; j < kTreeTile; j += 32) {
+                for (int k = 0; k < 2; ++k) {
+                    const int j = lane + 32 * k;
                     float x;
                     asm volatile("ld.shared.f32 %0, [%1];"
                                  : "=f"(x)
                                  : "r"(raw + (j / BS) * C::kBlockBytes + BS * D + (j % BS) * 4)
                                  : "memory");
-                    scales[j] = x;
-                    if (j < left && x < INFINITY)
-                        top = fmaxf(top, x);
+                    if (is_v) {
+                        x = j < left ? x : 0.f;
+                        const bool fine = fabsf(x) < INFINITY;
+                        odd[k] = __ballot_sync(0xffffffffu, !fine);
+                        top = fine ? fmaxf(top, x) : top;
+                        scales[j] = fine ? x : 1.f;
+                    } else {
+                        scales[j] = x * p.qk_scale_log2;
+                    }
                 }
                 if (is_v) {
                     for (int o = 16; o > 0; o >>= 1)
@@ -550,20 +568,27 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                 for (int u = 0; u < 2; ++u)
                     at[q][u] = ring + st * C::kTileBytes +
                                tree_piece_at<D>(q * kRows + r0, 2 * i + (turn ? 1 - u : u));
+            const bool bf16 = !is_v && std::is_same<QT, __nv_bfloat16>::value;
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b) {
                 const uint32_t from = raw + b * C::kBlockBytes + lane * 16;
+                // All of a block's loads before its stores, for their latency.
+                uint4 codes[BS / kRows];
 #pragma unroll
                 for (int r = 0; r < BS; r += kRows) {
-                    uint4 code;
+                    uint4 &code = codes[r / kRows];
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                  : "=r"(code.x), "=r"(code.y), "=r"(code.z), "=r"(code.w)
                                  : "r"(from + r * D)
                                  : "memory");
+                }
+#pragma unroll
+                for (int r = 0; r < BS; r += kRows) {
+                    const uint4 code = codes[r / kRows];
                     uint32_t w[8];
                     Store<E4M3>::to_h2(turn ? make_uint4(code.z, code.w, code.x, code.y) : code,
                                        w);
-                    if (std::is_same<QT, __nv_bfloat16>::value) {
+                    if (bf16) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float2 f = h2_to_float2(w[e]);
@@ -578,6 +603,30 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                                      "r"(w[4 * u]), "r"(w[4 * u + 1]), "r"(w[4 * u + 2]),
                                      "r"(w[4 * u + 3])
                                      : "memory");
+                }
+            }
+            for (uint64_t rows = (uint64_t)odd[1] << 32 | odd[0]; rows; rows &= rows - 1) {
+                const int j = __ffsll((long long)rows) - 1;
+                const uint32_t tile_of = raw + (j / BS) * C::kBlockBytes;
+                __syncwarp();
+                for (int e = lane; e < D; e += 32) {
+                    uint32_t code;
+                    float scale;
+                    asm volatile("ld.shared.u8 %0, [%1];"
+                                 : "=r"(code)
+                                 : "r"(tile_of + (j % BS) * D + e)
+                                 : "memory");
+                    asm volatile("ld.shared.f32 %0, [%1];"
+                                 : "=f"(scale)
+                                 : "r"(tile_of + BS * D + (j % BS) * 4)
+                                 : "memory");
+                    float f[4];
+                    e4m3x4_to_float(code, f);
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(ring + st * C::kTileBytes +
+                                                                 tree_piece_at<D>(j, e / 8) +
+                                                                 e % 8 * 2),
+                                 "h"((uint16_t)pack2<typename C::PT>(f[0] * scale, 0.f))
+                                 : "memory");
                 }
             }
             fence_proxy_async_smem();
@@ -729,6 +778,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
     using C = TreeCfg<T, D, BS>;
     constexpr int NS = C::kStages;
     constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
+    using PT = typename C::PT;
     extern __shared__ __align__(1024) uint8_t tree_dyn[];
     __shared__ TreeShared<NS> sh;
     const TreeDecodeParams &p = g.p;
@@ -767,7 +817,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
         sh.keep_o = -1;
         sh.strange[0] = sh.strange[1] = 0;
     }
-    if (warp == kSoftmaxWarps + 2)
+    if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sh.tmem), C::kColumns);
     tcgen05_fence_before();
     pdl_wait_prior_grid();
@@ -783,15 +833,16 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
     if (sh.plan.empty) {
         if (tid == 0)
             p.ws_records[blockIdx.x].parts = 0;
-    } else if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 1) {
-        const bool is_v = warp != kSoftmaxWarps;
+    } else if (warp == kFetchKWarp || warp == kFetchVWarp) {
+        const bool is_v = warp == kFetchVWarp;
         tree_fetch<T, QT, D, BS>(g, is_v, sh, q_tile, is_v ? v_tiles : k_tiles,
                                  raw_tiles + (is_v ? kRawStages * C::kRawBytes : 0), ok);
-    } else if (warp == kSoftmaxWarps + 2) {
+    } else if (warp == kMmaWarp) {
         // --- MMAs: the warp waits together, one lane issues ---------------------------------
         const uint32_t idesc_qk =
             umma_idesc(kBf16, false, kTreeRows, kTreeTile) | (p.negate ? kUmmaNegateA : 0);
-        constexpr uint32_t kIdescPv = umma_idesc(kBf16, true, kTreeRows, D);
+        constexpr uint32_t kIdescPv =
+            umma_idesc(std::is_same<PT, __nv_bfloat16>::value, true, kTreeRows, D);
         const auto wait_warp = [&](uint64_t &bar, uint32_t parity) {
             ok = __all_sync(0xffffffffu, wait(bar, parity));
             return ok;
@@ -871,7 +922,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
             __syncwarp();
             mbar_wait_bounded(smem_addr(&sh.drain), 0, kWaitLimitNs);
         }
-    } else {
+    } else if (warp < kSoftmaxWarps) {
         // --- softmax, one thread per row ----------------------------------------------------
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const uint32_t o_column = tmem + lanes;
@@ -972,7 +1023,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                                          : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                                          : "r"(at)
                                          : "memory");
-                            bad |= not_finite<QT>(x);
+                            bad |= not_finite<PT>(x);
                         }
                     }
                     if (bad)
@@ -996,36 +1047,39 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
 #pragma unroll
                     for (int k = 0; k < NC; k += 32)
                         tmem_ld_x32(s_column + k, x + k);
-                    float factor = c;
-                    [[maybe_unused]] float inv_R = 0.f;
+                    float factor = c, log2_R = 0.f;
+                    [[maybe_unused]] float unit_R = 1.f;
                     if constexpr (C::kFp8) {
                         const float4 *ks = reinterpret_cast<const float4 *>(sh.ks[it & 3]);
 #pragma unroll
                         for (int k = 0; k < NC / 4; ++k) {
-                            const float4 s4 = ks[k];
-                            const float f[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const float2 y = mul_f32x2(
-                                    make_float2(__uint_as_float(x[4 * k + e]),
-                                                __uint_as_float(x[4 * k + e + 1])),
-                                    mul_f32x2(make_float2(f[e], f[e + 1]), make_float2(c, c)));
-                                x[4 * k + e] = __float_as_uint(y.x);
-                                x[4 * k + e + 1] = __float_as_uint(y.y);
-                            }
+                            const float4 f = ks[k];
+                            const float2 y = mul_f32x2(make_float2(__uint_as_float(x[4 * k]),
+                                                                   __uint_as_float(x[4 * k + 1])),
+                                                       make_float2(f.x, f.y));
+                            const float2 z =
+                                mul_f32x2(make_float2(__uint_as_float(x[4 * k + 2]),
+                                                      __uint_as_float(x[4 * k + 3])),
+                                          make_float2(f.z, f.w));
+                            x[4 * k] = __float_as_uint(y.x);
+                            x[4 * k + 1] = __float_as_uint(y.y);
+                            x[4 * k + 2] = __float_as_uint(z.x);
+                            x[4 * k + 3] = __float_as_uint(z.y);
                         }
                         factor = 1.f;
-                        // V's scales relative to R, the power of two above
-                        // the largest so far: p * scale / R stays in f16's
-                        // range whatever the scales.
+                        // Weights are p * scale / R, R the power of two
+                        // above the largest V scale so far: in f16's range
+                        // whatever the scales. 1 / R goes into the exponent.
                         float top_v = sh.vmax[it & 3];
                         if (kMasked) {
                             top_v = 0.f;
-#pragma unroll 1
-                            for (int k = 0; k < NC; ++k) {
-                                const float v = sh.vs[it & 3][k];
-                                if (((seen >> k) & 1) && v < INFINITY)
-                                    top_v = fmaxf(top_v, v);
+#pragma unroll 2
+                            for (int k = 0; k < NC; k += 4) {
+                                const float4 v =
+                                    *reinterpret_cast<const float4 *>(&sh.vs[it & 3][k]);
+                                const uint32_t b = (uint32_t)(seen >> k);
+                                top_v = max3(top_v, b & 1 ? v.x : 0.f, b & 2 ? v.y : 0.f);
+                                top_v = max3(top_v, b & 4 ? v.z : 0.f, b & 8 ? v.w : 0.f);
                             }
                         }
                         if (top_v > R) {
@@ -1036,7 +1090,9 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                             rescale = tile > d.tile0;
                             R = up2;
                         }
-                        inv_R = R > 0.f ? 1.f / R : 0.f;
+                        const int e = (int)(__float_as_uint(R) >> 23); // 0: only zero scales yet
+                        log2_R = e ? (float)(e - 127) : 0.f;
+                        unit_R = e ? R : 1.f;
                     }
                     if (kMasked) {
 #pragma unroll
@@ -1063,7 +1119,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         rescale = tile > d.tile0;
                         m = top;
                     }
-                    const float off = kTreeBias - (m == -INFINITY ? 0.f : m);
+                    const float off = kTreeBias - (m == -INFINITY ? 0.f : m) - log2_R;
                     const float2 c2 = make_float2(factor, factor), off2 = make_float2(off, off);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1075,17 +1131,16 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         w.y = ex2(w.y);
                         sum[k & 1] = add_f32x2(sum[k & 1], w);
                         if constexpr (C::kFp8) {
-                            float2 v = *reinterpret_cast<const float2 *>(&sh.vs[it & 3][2 * k]);
-                            if (kMasked) { // what is not seen may be NaN
-                                v.x = (seen >> (2 * k)) & 1 ? v.x : 0.f;
-                                v.y = (seen >> (2 * k + 1)) & 1 ? v.y : 0.f;
-                            }
-                            w = mul_f32x2(w, mul_f32x2(v, make_float2(inv_R, inv_R)));
+                            const float4 v4 =
+                                reinterpret_cast<const float4 *>(sh.vs[it & 3])[k >> 1];
+                            w = mul_f32x2(w, k & 1 ? make_float2(v4.z, v4.w)
+                                                   : make_float2(v4.x, v4.y));
                         }
-                        x[k] = pack2<QT>(w.x, w.y); // in place: pair k is done with x[2k..]
+                        x[k] = pack2<PT>(w.x, w.y); // in place: pair k is done with x[2k..]
                     }
                     sum[0] = add_f32x2(sum[0], sum[1]);
-                    l = fmaf(l, keep, sum[0].x + sum[0].y);
+                    const float more = sum[0].x + sum[0].y;
+                    l = fmaf(l, keep, C::kFp8 ? more * unit_R : more);
                 };
                 if (warp_live) {
                     if (special)
@@ -1128,7 +1183,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                     }
                     if (warp_live) {
                         const int nodes = d.n - t0; // rows behind are just emptied
-                        rescue_rows<QT, D>(nodes < 64 ? strange & ((1ull << nodes) - 1) : strange,
+                        rescue_rows<PT, D>(nodes < 64 ? strange & ((1ull << nodes) - 1) : strange,
                                            seen, v_tile, s_column, o_column);
                     }
                     if (!sync_warps())
@@ -1221,7 +1276,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
         report(p.dev_err, PA_DEVERR_TIMEOUT);
     tcgen05_fence_before();
     __syncthreads();
-    if (warp == kSoftmaxWarps + 2) {
+    if (warp == kMmaWarp) {
         tcgen05_fence_after();
         tmem_dealloc(tmem, C::kColumns);
     }
