@@ -11,8 +11,9 @@ Cache tensors are [num_blocks, num_heads, block_size, head_dim] fp16/bf16
 """
 from __future__ import annotations
 
-import contextlib
+import array
 import ctypes
+import operator
 import os
 
 import torch
@@ -129,9 +130,8 @@ _lib.pa_tree_decode.argtypes = [_P, ctypes.c_int, _P, _i32, _i32, _i32, _P, _P,
 _lib.pa_tree_accept.restype = ctypes.c_int
 _lib.pa_tree_accept.argtypes = [_P, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _P, _P]
 _lib.pa_tree_compact.restype = ctypes.c_int
-_lib.pa_tree_compact.argtypes = [ctypes.POINTER(_P), ctypes.POINTER(_P), _i32,
-                                 ctypes.POINTER(CacheDesc), _P, _i32, _P, _P, _P, _i32, _i32, _P,
-                                 _P]
+_lib.pa_tree_compact.argtypes = [_P, _P, _i32, ctypes.POINTER(CacheDesc), _P, _i32, _P, _P, _P,
+                                 _i32, _i32, _P, _P]
 _lib.pa_selftest_wait_timeout.restype = ctypes.c_int
 _lib.pa_selftest_wait_timeout.argtypes = [_P, ctypes.c_uint32, _P]
 _lib.pa_status_string.restype = ctypes.c_char_p
@@ -393,36 +393,79 @@ def swap_blocks(src_key_caches, src_value_caches, dst_key_caches, dst_value_cach
                                L, _ptr(block_mapping), n, _ptr(dev_err), stream))
 
 
-def _on_device(device):
-    """Launches go to the current device: the tensors' own, for the call."""
-    if device.index == torch.cuda.current_device():
-        return _HERE_ALREADY
-    return torch.cuda.device(device)
+# The tree calls are made once a layer or once a step on little data, so their
+# checks are written for speed: device indices instead of device objects, the
+# raw stream, no context manager unless the tensors are on another device than
+# the current one.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
-_HERE_ALREADY = contextlib.nullcontext()
+def _call(fn, device: int, *args):
+    """``fn(*args, stream)`` on the tensors' own device and its current stream."""
+    if device == _current_device():
+        status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
+    if status:
+        _check(status)
 
 
-def _need_vector(t, name, dtype, size, device):
-    _need(t, name, dtype)
-    if t.dim() != 1 or (size is not None and t.shape[0] != size):
-        raise ValueError(f"{name} must have shape [{'' if size is None else size}]")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+def _refuse(t, name, dtype, device, shape):
+    """The error for a tensor that is not what the two checks below want."""
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        return ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        return ValueError(f"{name} must be contiguous")
+    if device is not None and t.get_device() != device:
+        return ValueError(f"{name} is on {t.device}, not cuda:{device}")
+    return ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _sized(t, name, dtype, device, shape):
+    """A contiguous tensor of a type and shape on CUDA device `device`."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or \
+            not t.is_contiguous():
+        raise _refuse(t, name, dtype, device, shape)
+
+
+def _matrix(t, name, dtype, device, rows):
+    """The same with two dimensions and any number of columns, which it returns."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or t.dtype != dtype or t.get_device() != device or \
+            not t.is_contiguous():
+        raise _refuse(t, name, dtype, device, (rows, "*"))
+    return shape[1]
+
+
+def _first(t, name, dtype, dim):
+    """A contiguous CUDA tensor of a type and number of dimensions, the first
+    of its call: its shape and device."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != dim or not t.is_cuda or not t.is_contiguous():
+        raise _refuse(t, name, dtype, None, ("*",) * dim)
+    return shape, t.get_device()
+
+
+def _err_ptr(dev_err, device):
+    if dev_err is None:
+        return None
+    _need(dev_err, "dev_err", torch.int32)
+    if dev_err.numel() < 1 or dev_err.get_device() != device:
+        raise ValueError(f"dev_err must be an int32 word on cuda:{device}")
+    return dev_err.data_ptr()
 
 
 def _num_trees(tree_start, device):
-    _need_vector(tree_start, "tree_start", torch.int32, None, device)
-    if tree_start.shape[0] < 1:
+    n = tree_start.numel()
+    if n < 1:
         raise ValueError("tree_start must have one entry more than there are sequences")
-    return tree_start.shape[0] - 1
-
-
-def _need_err(dev_err, device):
-    if dev_err is not None:
-        _need(dev_err, "dev_err", torch.int32)
-        if dev_err.numel() < 1 or dev_err.device != device:
-            raise ValueError(f"dev_err must be an int32 word on {device}")
+    _sized(tree_start, "tree_start", torch.int32, device, (n,))
+    return n - 1
 
 
 def tree_mask(mask, depth, parents, tree_start, dev_err=None):
@@ -431,19 +474,14 @@ def tree_mask(mask, depth, parents, tree_start, dev_err=None):
     j % 32 of word j // 32: node j is the row's node or an ancestor of it)
     and ``depth`` int32 [N] (or None). Trees have at most 32 * W nodes. Rows
     of no tree are left as they were."""
-    _need(parents, "parents", torch.int32)
-    dev, N = parents.device, parents.numel()
-    _need_vector(parents, "parents", torch.int32, None, dev)
+    i32 = torch.int32
+    (N,), dev = _first(parents, "parents", i32, 1)
     S = _num_trees(tree_start, dev)
-    _need(mask, "mask", torch.int32)
-    if mask.dim() != 2 or mask.shape[0] != N or mask.device != dev:
-        raise ValueError(f"mask must be [{N}, words] on {dev}")
+    words = _matrix(mask, "mask", i32, dev, N)
     if depth is not None:
-        _need_vector(depth, "depth", torch.int32, N, dev)
-    _need_err(dev_err, dev)
-    with _on_device(dev):
-        _check(_lib.pa_tree_mask(_ptr(mask), _ptr(depth), _ptr(parents), _ptr(tree_start), S, N,
-                                 mask.shape[1], _ptr(dev_err), _stream(parents)))
+        _sized(depth, "depth", i32, dev, (N,))
+    _call(_lib.pa_tree_mask, dev, mask.data_ptr(), _ptr(depth), parents.data_ptr(),
+          tree_start.data_ptr(), S, N, words, _err_ptr(dev_err, dev))
     return mask, depth
 
 
@@ -460,7 +498,7 @@ def tree_decode_workspace_size(cache):
 def alloc_tree_workspace(cache):
     """A workspace for :func:`tree_decode` over ``cache`` (and any other cache
     of its head dimension), on its device. Needs no initialisation."""
-    with _on_device(cache.device):
+    with torch.cuda.device(cache.device):
         return torch.empty(tree_decode_workspace_size(cache), dtype=torch.uint8,
                            device=cache.device)
 
@@ -474,41 +512,41 @@ def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, 
     :func:`tree_mask`); node j's K/V are at position context_lens[s] + j.
     ``out`` may be fp16, bf16 or fp32; ``workspace`` is allocated here when
     not given."""
+    i32 = torch.int32
     _need_cache(key_cache, "key_cache")
     _need_cache(value_cache, "value_cache", key_cache)
-    _need(query, "query", io_dtype(key_cache))
-    _need(out, "out")
-    if out.dtype not in _DTYPE:
+    desc, row = cache_desc(key_cache), io_dtype(key_cache)
+    if isinstance(key_cache, Fp8Cache):
+        dev = key_cache.data.get_device()
+        if value_cache.io_dtype != row or value_cache.data.get_device() != dev or \
+                value_cache.block_size != key_cache.block_size:
+            raise ValueError("value_cache does not match the other cache")
+    else:
+        dev = key_cache.get_device()
+        if value_cache.get_device() != dev:
+            raise ValueError("value_cache does not match the other cache")
+    (N, H, D), on = _first(query, "query", row, 3)
+    if on != dev:
+        raise ValueError(f"query is on {query.device}, not cuda:{dev}")
+    kind = _DTYPE.get(out.dtype)
+    if kind is None:
         raise ValueError("out dtype must be float16, bfloat16 or float32")
-    desc, dev = cache_desc(key_cache), key_cache.device
-    if query.dim() != 3 or out.shape != query.shape or query.shape[2] != desc.head_dim:
+    _sized(out, "out", out.dtype, dev, (N, H, D))
+    if D != desc.head_dim:
         raise ValueError(f"query and out must be [N, H, {desc.head_dim}]")
-    N, H, _ = query.shape
     S = _num_trees(tree_start, dev)
-    _need_vector(context_lens, "context_lens", torch.int32, S, dev)
-    _need(block_tables, "block_tables", torch.int32)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError(f"block_tables must be [{S}, blocks]")
-    _need(mask, "mask", torch.int32)
-    if mask.dim() != 2 or mask.shape[0] != N:
-        raise ValueError(f"mask must be [{N}, words]")
-    for t in (value_cache, query, out, block_tables, mask):
-        if t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}")
-    _need_err(dev_err, dev)
+    _sized(context_lens, "context_lens", i32, dev, (S,))
+    width = _matrix(block_tables, "block_tables", i32, dev, S)
+    words = _matrix(mask, "mask", i32, dev, N)
     if workspace is None:
         workspace = alloc_tree_workspace(key_cache)
-    _need(workspace, "workspace")
-    if workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
-    with _on_device(dev):
-        _check(_lib.pa_tree_decode(_ptr(out), _DTYPE[out.dtype], _ptr(query), S, N, H,
-                                   _ptr(key_cache), _ptr(value_cache), ctypes.byref(desc),
-                                   _ptr(block_tables), block_tables.shape[1],
-                                   _ptr(context_lens), _ptr(tree_start), _ptr(mask),
-                                   mask.shape[1], float(scale), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _ptr(dev_err),
-                                   _stream(query)))
+    elif not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    _call(_lib.pa_tree_decode, dev, out.data_ptr(), kind, query.data_ptr(), S, N, H,
+          key_cache.data_ptr(), value_cache.data_ptr(), desc, block_tables.data_ptr(), width,
+          context_lens.data_ptr(), tree_start.data_ptr(), mask.data_ptr(), words, scale,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          _err_ptr(dev_err, dev))
     return out
 
 
@@ -520,23 +558,18 @@ def tree_accept(accepted, accepted_lens, next_token, parents, tree_start, draft_
     ``accepted`` int32 [S, max_path] (-1 past the path), ``accepted_lens``
     int32 [S] and ``next_token`` int64 [S], the model's token at the path's
     last node. A path is cut at max_path nodes."""
-    _need(parents, "parents", torch.int32)
-    dev, N = parents.device, parents.numel()
-    _need_vector(parents, "parents", torch.int32, None, dev)
+    i32, i64 = torch.int32, torch.int64
+    (N,), dev = _first(parents, "parents", i32, 1)
     S = _num_trees(tree_start, dev)
-    _need_vector(draft_tokens, "draft_tokens", torch.int64, N, dev)
-    _need_vector(target_tokens, "target_tokens", torch.int64, N, dev)
-    _need(accepted, "accepted", torch.int32)
-    if accepted.dim() != 2 or accepted.shape[0] != S or accepted.device != dev:
-        raise ValueError(f"accepted must be [{S}, max_path] on {dev}")
-    _need_vector(accepted_lens, "accepted_lens", torch.int32, S, dev)
-    _need_vector(next_token, "next_token", torch.int64, S, dev)
-    _need_err(dev_err, dev)
-    with _on_device(dev):
-        _check(_lib.pa_tree_accept(_ptr(accepted), _ptr(accepted_lens), _ptr(next_token),
-                                   _ptr(parents), _ptr(tree_start), _ptr(draft_tokens),
-                                   _ptr(target_tokens), S, N, accepted.shape[1], _ptr(dev_err),
-                                   _stream(parents)))
+    _sized(draft_tokens, "draft_tokens", i64, dev, (N,))
+    _sized(target_tokens, "target_tokens", i64, dev, (N,))
+    room = _matrix(accepted, "accepted", i32, dev, S)
+    _sized(accepted_lens, "accepted_lens", i32, dev, (S,))
+    _sized(next_token, "next_token", i64, dev, (S,))
+    _call(_lib.pa_tree_accept, dev, accepted.data_ptr(), accepted_lens.data_ptr(),
+          next_token.data_ptr(), parents.data_ptr(), tree_start.data_ptr(),
+          draft_tokens.data_ptr(), target_tokens.data_ptr(), S, N, room,
+          _err_ptr(dev_err, dev))
     return accepted, accepted_lens, next_token
 
 
@@ -545,33 +578,37 @@ def tree_compact(key_caches, value_caches, block_tables, context_lens, accepted,
     """Move the accepted nodes' K/V rows behind the context, in place and in
     every layer: position context_lens[s] + accepted[s, k] to position
     context_lens[s] + k for k < accepted_lens[s]."""
-    if len(key_caches) != len(value_caches) or not key_caches:
+    L = len(key_caches)
+    if len(value_caches) != L or not L:
         raise ValueError("need the same, non-zero number of K and V caches")
+    i32 = torch.int32
     like = key_caches[0]
-    dev = like.device
-    for caches in (key_caches, value_caches):
-        for c in caches:
-            _need_cache(c, "cache", like)
-            if c.device != dev:
-                raise ValueError(f"all caches must be on {dev}")
-    desc, L = cache_desc(like), len(key_caches)
-    _need(accepted, "accepted", torch.int32)
-    if accepted.dim() != 2 or accepted.device != dev:
-        raise ValueError(f"accepted must be [sequences, max_path] on {dev}")
-    S = accepted.shape[0]
-    _need_vector(accepted_lens, "accepted_lens", torch.int32, S, dev)
-    _need_vector(context_lens, "context_lens", torch.int32, S, dev)
-    _need(block_tables, "block_tables", torch.int32)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or block_tables.device != dev:
-        raise ValueError(f"block_tables must be [{S}, blocks] on {dev}")
-    _need_err(dev_err, dev)
-    kp = (_P * L)(*[c.data_ptr() for c in key_caches])
-    vp = (_P * L)(*[c.data_ptr() for c in value_caches])
-    with _on_device(dev):
-        _check(_lib.pa_tree_compact(kp, vp, L, ctypes.byref(desc), _ptr(block_tables),
-                                    block_tables.shape[1], _ptr(context_lens), _ptr(accepted),
-                                    _ptr(accepted_lens), S, accepted.shape[1], _ptr(dev_err),
-                                    _stream(like.data if isinstance(like, Fp8Cache) else like)))
+    _need_cache(like, "cache")
+    desc = cache_desc(like)
+    caches = [*key_caches, *value_caches]
+    if isinstance(like, Fp8Cache):
+        if any(not isinstance(c, Fp8Cache) or c.block_size != like.block_size for c in caches):
+            raise ValueError("cache does not match the other cache")
+        caches, like = [c.data for c in caches], like.data
+    elif any(isinstance(c, Fp8Cache) for c in caches):
+        raise ValueError("cache does not match the other cache")
+    # A list at a time: with 32 layers these checks are most of the call.
+    T, dev = torch.Tensor, like.get_device()
+    if set(map(_dtype_of, caches)) != {like.dtype} or set(map(T.get_device, caches)) != {dev} or \
+            list(map(_shape_of, caches)).count(like.shape) != 2 * L:
+        raise ValueError("cache does not match the other cache")
+    if not all(map(T.is_contiguous, caches)):
+        raise ValueError("cache must be contiguous")
+    pointers = array.array("Q", map(T.data_ptr, caches))
+    S = accepted.shape[0] if accepted.dim() else 0
+    room = _matrix(accepted, "accepted", i32, dev, S)
+    _sized(accepted_lens, "accepted_lens", i32, dev, (S,))
+    _sized(context_lens, "context_lens", i32, dev, (S,))
+    width = _matrix(block_tables, "block_tables", i32, dev, S)
+    at = pointers.buffer_info()[0]
+    _call(_lib.pa_tree_compact, dev, at, at + 8 * L, L, desc, block_tables.data_ptr(), width,
+          context_lens.data_ptr(), accepted.data_ptr(), accepted_lens.data_ptr(), S, room,
+          _err_ptr(dev_err, dev))
 
 
 def selftest_wait_timeout(limit_us: int = 1000, device="cuda") -> int:
