@@ -156,6 +156,7 @@ struct TreePlan {
     int64_t unit_begin;      // first place of the unit that `begin` is in
     int32_t seq, unit, tile; // that unit, and the piece's first tile of it
     bool empty;              // no tile in this piece
+    TreeSeq q;               // that sequence
 
     __device__ __forceinline__ int64_t piece(int b) const
     {
@@ -167,8 +168,9 @@ struct TreePlan {
         return (int)max((int64_t)0, min((int64_t)tiles, end - first_place - kTreeUnitCost));
     }
     // The thread whose sequence q, beginning at `first`, holds `begin`.
-    __device__ __forceinline__ void locate(const TreeSeq &q, int s, int64_t first)
+    __device__ __forceinline__ void locate(const TreeSeq &at, int s, int64_t first)
     {
+        q = at;
         const int places = q.tiles + kTreeUnitCost;
         seq = s;
         unit = (int)((begin - first) / places);
@@ -503,7 +505,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     const CUtensorMap *map = is_v ? &g.v : &g.k;
     const uint8_t *pool = static_cast<const uint8_t *>(is_v ? p.value_cache : p.key_cache);
     int s = sh.plan.seq;
-    TreeSeq q = tree_seq(p, s, BS);
+    TreeSeq q = sh.plan.q;
     int64_t unit_begin = sh.plan.unit_begin;
     int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
     // Widens tile `of` of the CTA, the first `blocks` blocks of which came.
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
             const TreePlan &plan = sh.plan;
             TreeMergeRecord rec = {0, 0, 0, 0};
             if (plan.tile > 0 && plan.piece(blockIdx.x - 1) <= plan.unit_begin + kTreeUnitCost) {
-                const TreeSeq q = tree_seq(p, plan.seq, BS);
+                const TreeSeq &q = plan.q;
                 const int64_t unit_last = plan.unit_begin + kTreeUnitCost + q.tiles - 1;
                 int e = blockIdx.x, hi = plan.ctas - 1; // the CTA with the unit's last tile
                 while (e < hi) {
@@ -1282,80 +1284,130 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
     }
 }
 
-// Joins the parts of the unit that is cut before CTA blockIdx.x, if there is
-// one and no earlier cut in it: O = sum_p 2^(m_p - M) acc_p / sum_p
-// 2^(m_p - M) l_p. A thread has one row and kMergeCols columns of four.
-constexpr int kMergeCols = 2;
+// Joins the parts of the unit that is cut before CTA blockIdx.x + 1, if there
+// is one and no earlier cut in it: O = sum_p 2^(m_p - M) acc_p / sum_p
+// 2^(m_p - M) l_p. A thread has one row and kMergeCols columns of four; a unit
+// in more than kMergeFew parts and of up to 32 (64) rows has four (two)
+// threads a row, each with every fourth (second) part, whose sums meet in
+// shared memory. Bound by the latency of its loads, a chunk of parts at a
+// time, and by the number of CTAs that the launch brings: one 2000-token
+// sequence of 8 K/V heads (up to 33 parts a unit) takes 13.0 us in all, 16.7
+// with one thread a row and two columns each; blocks of 512 threads, which
+// find no room beside the CTAs of the kernel before, 15.0.
+constexpr int kMergeCols = 4, kMergeFew = 4;
+
+struct TreeMergeSum {
+    float m, l;
+    float4 o[kMergeCols];
+    bool saw;
+
+    __device__ __forceinline__ void rescale(float to)
+    {
+        const float use = to == -INFINITY ? 0.f : to, keep = ex2(m - use);
+        m = to;
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < kMergeCols; ++k)
+            o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kTreeRows) tree_merge_kernel(
     const __grid_constant__ TreeDecodeParams p)
 {
+    __shared__ TreeMergeSum other[96];
     pdl_launch_dependents();
     pdl_wait_prior_grid();
     const int b = blockIdx.x + 1;
     const TreeMergeRecord rec = p.ws_records[b];
-    const int row = threadIdx.x;
-    if (rec.parts == 0 || row >= rec.rows)
+    if (rec.parts == 0)
         return;
-    const auto slot = [&](int i) { return i == 0 ? (size_t)(b - 1) * 2 + 1 : (size_t)(b + i - 1) * 2; };
-    constexpr int kCols = kMergeCols, kChunk = 4; // parts whose loads are in flight together
-    const int c0 = blockIdx.y * kCols;
-    float M = -INFINITY, L = 0.f;
-    bool saw = false;
-    float4 o[kCols];
+    // Threads of a group.
+    const int span = rec.parts <= kMergeFew || rec.rows > 64 ? 128 : rec.rows > 32 ? 64 : 32;
+    const int row = threadIdx.x % span, grp = threadIdx.x / span, groups = kTreeRows / span;
+    const auto slot = [&](int i) {
+        return i == 0 ? (size_t)(b - 1) * 2 + 1 : (size_t)(b + i - 1) * 2;
+    };
+    constexpr int kChunk = 4; // parts whose loads are in flight together
+    const int c0 = blockIdx.y * kMergeCols;
+    TreeMergeSum sum;
+    sum.m = -INFINITY;
+    sum.l = 0.f;
+    sum.saw = false;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
-        o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < rec.parts; i0 += kChunk) {
+    for (int k = 0; k < kMergeCols; ++k)
+        sum.o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = grp; row < rec.rows && i0 < rec.parts; i0 += kChunk * groups) {
         float2 ml[kChunk];
-        float4 a[kChunk][kCols];
+        float4 a[kChunk][kMergeCols];
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
             ml[i] = make_float2(-INFINITY, 0.f);
-            if (i0 + i < rec.parts) {
-                const size_t at = slot(i0 + i);
+            if (i0 + i * groups < rec.parts) {
+                const size_t at = slot(i0 + i * groups);
                 ml[i] = __ldcg(p.ws_ml + at * kTreeRows + row);
 #pragma unroll
-                for (int k = 0; k < kCols; ++k)
+                for (int k = 0; k < kMergeCols; ++k)
                     a[i][k] = __ldcg(p.ws_acc + (at * (D / 4) + c0 + k) * kTreeRows + row);
             }
         }
-        float top = M;
+        float top = sum.m;
 #pragma unroll
         for (int i = 0; i < kChunk; ++i)
             top = fmaxf(top, ml[i].x);
-        const float use = top == -INFINITY ? 0.f : top, keep = ex2(M - use);
-        M = top;
-        L *= keep;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k)
-            o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
+        sum.rescale(top);
+        const float use = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
-            if (i0 + i >= rec.parts)
+            if (i0 + i * groups >= rec.parts)
                 break;
             const float w = ex2(ml[i].x - use);
-            saw |= ml[i].y != 0.f || signbit(ml[i].y);
-            L = fmaf(ml[i].y, w, L);
+            sum.saw |= ml[i].y != 0.f || signbit(ml[i].y);
+            sum.l = fmaf(ml[i].y, w, sum.l);
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                o[k].x = fmaf(a[i][k].x, w, o[k].x);
-                o[k].y = fmaf(a[i][k].y, w, o[k].y);
-                o[k].z = fmaf(a[i][k].z, w, o[k].z);
-                o[k].w = fmaf(a[i][k].w, w, o[k].w);
+            for (int k = 0; k < kMergeCols; ++k) {
+                sum.o[k].x = fmaf(a[i][k].x, w, sum.o[k].x);
+                sum.o[k].y = fmaf(a[i][k].y, w, sum.o[k].y);
+                sum.o[k].z = fmaf(a[i][k].z, w, sum.o[k].z);
+                sum.o[k].w = fmaf(a[i][k].w, w, sum.o[k].w);
             }
         }
     }
-    const bool none = L == 0.f && !saw;
-    const float inv = none ? 0.f : 1.f / L;
+    if (groups > 1) {
+        if (grp > 0)
+            other[(int)threadIdx.x - span] = sum;
+        __syncthreads();
+        if (grp > 0)
+            return;
+        for (int g = 1; g < groups; ++g) {
+            TreeMergeSum x = other[(g - 1) * span + row];
+            const float top = fmaxf(sum.m, x.m);
+            sum.rescale(top);
+            x.rescale(top);
+            sum.l += x.l;
+            sum.saw |= x.saw;
+#pragma unroll
+            for (int k = 0; k < kMergeCols; ++k) {
+                sum.o[k].x += x.o[k].x;
+                sum.o[k].y += x.o[k].y;
+                sum.o[k].z += x.o[k].z;
+                sum.o[k].w += x.o[k].w;
+            }
+        }
+    }
+    if (row >= rec.rows)
+        return;
+    const bool none = sum.l == 0.f && !sum.saw;
+    const float inv = none ? 0.f : 1.f / sum.l;
     const int node = row / p.group;
     const size_t at = ((size_t)(rec.first_row + node) * p.num_heads + rec.kv_head * p.group +
                        (row - node * p.group)) * D + c0 * 4;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k)
+    for (int k = 0; k < kMergeCols; ++k)
         store_row4(p.out, p.out_dtype, at + 4 * k,
-                   make_float4(none ? 0.f : o[k].x * inv, none ? 0.f : o[k].y * inv,
-                               none ? 0.f : o[k].z * inv, none ? 0.f : o[k].w * inv));
+                   make_float4(none ? 0.f : sum.o[k].x * inv, none ? 0.f : sum.o[k].y * inv,
+                               none ? 0.f : sum.o[k].z * inv, none ? 0.f : sum.o[k].w * inv));
 }
 
 } // namespace pagedkv
