@@ -76,11 +76,12 @@ constexpr int kTreeUnitCost = PA_TREE_UNIT_COST;
 constexpr float kTreeSlack = 6.f;
 constexpr float kTreeBias = 8.f;
 
-// Where a unit cut between CTAs b-1 and b (and not before) has its parts:
-// part 0 in CTA b-1's second slot, parts 1 .. parts-1 in the first slots of
-// CTAs b .. b+parts-2.
+// Where a unit cut before CTA b's piece (and not earlier) has its parts: part
+// 0 in the second slot of the CTA with the piece before, parts 1 .. parts-1
+// in the first slots of b and the CTAs with the pieces after.
 struct TreeMergeRecord {
-    int32_t parts; // 0: no unit to merge here
+    int32_t parts;  // 0: no unit to merge here
+    int32_t stride; // of CTAs from one piece to the next
     int32_t rows;
     int32_t first_row; // row of out of the tile's first node
     int32_t kv_head;
@@ -144,23 +145,24 @@ __device__ __forceinline__ int64_t tree_seq_places(const TreeDecodeParams &p, co
 }
 
 // What a CTA does. The line has kTreeUnitCost + tiles places per unit, and of
-// n = `ctas` pieces piece b begins at place b * total / n: the first
+// n = `pieces` pieces piece b begins at place b * total / n: the first
 // kTreeUnitCost places of a unit stand for its fixed cost (query rows, the
 // masked tiles at its end, the epilogue), so that a piece of many short units
 // takes as long as one of a few long ones. A piece that begins in them begins
 // with the unit's first tile.
 struct TreePlan {
     int64_t begin, end;      // places of the line
-    int64_t each;            // total / ctas
-    int32_t ctas, rest;      // rest: total % ctas
+    int32_t stride, lane;    // CTAs that share a piece, and which of them this is
+    int64_t each;            // total / pieces
+    int32_t pieces, rest;    // rest: total % pieces
     int64_t unit_begin;      // first place of the unit that `begin` is in
-    int32_t seq, unit, tile; // that unit, and the piece's first tile of it
+    int32_t seq, unit, tile; // that unit of the sequence, and the piece's first tile of it
     bool empty;              // no tile in this piece
     TreeSeq q;               // that sequence
 
     __device__ __forceinline__ int64_t piece(int b) const
     {
-        return b * each + (uint32_t)(b * rest) / (uint32_t)ctas;
+        return b * each + (uint32_t)(b * rest) / (uint32_t)pieces;
     }
     // The end of this piece among the tiles of a unit.
     __device__ __forceinline__ int tile_end(int64_t first_place, int tiles) const
@@ -189,19 +191,26 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
     const int nwarps = blockDim.x >> 5;
     const bool one = p.num_seqs <= (int)blockDim.x; // the usual case: one sequence per thread
     int64_t total = 0, mine = 0, before = 0;
-    int32_t error = 0;
+    int32_t error = 0, odd = 0;
     TreeSeq q;
     for (int s0 = 0; s0 < p.num_seqs; s0 += blockDim.x) {
         const int s = s0 + tid;
         if (s < p.num_seqs) {
             q = tree_seq(p, s, bs);
             error |= q.error;
+            odd |= q.row_tiles & 1;
             mine = tree_seq_places(p, q);
             total += mine;
         }
     }
     if (error && blockIdx.x == 0)
         report(p.dev_err, error);
+    // Where every tree has an even number of row tiles, two CTAs share each
+    // piece, one for the even and one for the odd ones: both then read the
+    // same keys and values at the same time, and L2 once.
+    const int halve = __syncthreads_or(odd) ? 0 : 1, stride = 1 + halve;
+    mine >>= halve;
+    total >>= halve;
     int64_t upto = one ? mine : total; // inclusive sums over threads
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -217,19 +226,22 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
             before = total;
         total += sums[w];
     }
-    const int ctas = (int)min((int64_t)gridDim.x, total);
+    const int pieces = (int)min((int64_t)(gridDim.x >> halve), total);
+    const int piece = blockIdx.x >> halve;
     if (tid == 0) {
-        plan->ctas = ctas;
+        plan->pieces = pieces;
+        plan->stride = stride;
+        plan->lane = blockIdx.x & halve;
         plan->empty = true;
-        if ((int)blockIdx.x < ctas) {
-            plan->each = total / ctas;
-            plan->rest = (int)(total % ctas);
-            plan->begin = plan->piece(blockIdx.x);
-            plan->end = plan->piece(blockIdx.x + 1);
+        if (piece < pieces) {
+            plan->each = total / pieces;
+            plan->rest = (int)(total % pieces);
+            plan->begin = plan->piece(piece);
+            plan->end = plan->piece(piece + 1);
         }
     }
     __syncthreads();
-    if ((int)blockIdx.x >= ctas)
+    if (piece >= pieces)
         return;
     const int64_t begin = plan->begin;
     if (one) {
@@ -246,7 +258,7 @@ __device__ __forceinline__ void tree_plan(const TreeDecodeParams &p, int bs, Tre
         mine = 0;
         if (s0 + tid < p.num_seqs) {
             q = tree_seq(p, s0 + tid, bs);
-            mine = tree_seq_places(p, q);
+            mine = tree_seq_places(p, q) >> halve;
         }
         upto = mine;
         for (int o = 1; o < 32; o <<= 1) {
@@ -506,6 +518,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     const uint8_t *pool = static_cast<const uint8_t *>(is_v ? p.value_cache : p.key_cache);
     int s = sh.plan.seq;
     TreeSeq q = sh.plan.q;
+    const int stride = sh.plan.stride;
     int64_t unit_begin = sh.plan.unit_begin;
     int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
     // Widens tile `of` of the CTA, the first `blocks` blocks of which came.
@@ -641,7 +654,8 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     uint32_t q_seen[2] = {0, 0}; // segments of each parity whose query rows were seen done
     bool was_whole = false;
     for (bool last = false; !last && ok; ++seg) {
-        const int rt = unit % q.row_tiles, h = unit / q.row_tiles;
+        const int row_tiles = q.row_tiles >> (stride - 1); // this CTA's
+        const int rt = unit % row_tiles * stride + sh.plan.lane, h = unit / row_tiles;
         const int tile0 = tile, end = sh.plan.tile_end(unit_begin, q.tiles);
         unit_begin += q.tiles + kTreeUnitCost;
         last = sh.plan.end <= unit_begin + kTreeUnitCost; // no tile of the next unit
@@ -746,7 +760,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
             break;
         // The next unit: of this sequence, or of the next one with any.
         tile = 0;
-        if (++unit == q.row_tiles * p.num_kv_heads && !last) {
+        if (++unit == row_tiles * p.num_kv_heads && !last) {
             unit = 0;
             for (++s; s < p.num_seqs; s += 32) {
                 const bool has = s + lane < p.num_seqs && tree_seq(p, s + lane, BS).nodes > 0;
@@ -944,11 +958,12 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
         if (tid == 0) {
             // The unit that this piece begins inside of, if it was cut here first.
             const TreePlan &plan = sh.plan;
-            TreeMergeRecord rec = {0, 0, 0, 0};
-            if (plan.tile > 0 && plan.piece(blockIdx.x - 1) <= plan.unit_begin + kTreeUnitCost) {
+            const int piece = blockIdx.x >> (plan.stride - 1);
+            TreeMergeRecord rec = {0, 0, 0, 0, 0};
+            if (plan.tile > 0 && plan.piece(piece - 1) <= plan.unit_begin + kTreeUnitCost) {
                 const TreeSeq &q = plan.q;
                 const int64_t unit_last = plan.unit_begin + kTreeUnitCost + q.tiles - 1;
-                int e = blockIdx.x, hi = plan.ctas - 1; // the CTA with the unit's last tile
+                int e = piece, hi = plan.pieces - 1; // the piece with the unit's last tile
                 while (e < hi) {
                     const int mid = (e + hi + 1) / 2;
                     if (plan.piece(mid) <= unit_last)
@@ -956,11 +971,13 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                     else
                         hi = mid - 1;
                 }
-                const int per_tile = kTreeRows / p.group, rt = plan.unit % q.row_tiles;
-                rec.parts = e - (int)blockIdx.x + 2;
+                const int per_tile = kTreeRows / p.group, row_tiles = q.row_tiles >> (plan.stride - 1);
+                const int rt = plan.unit % row_tiles * plan.stride + plan.lane;
+                rec.parts = e - piece + 2;
+                rec.stride = plan.stride;
                 rec.rows = min(per_tile, q.nodes - rt * per_tile) * p.group;
                 rec.first_row = q.first + rt * per_tile;
-                rec.kv_head = plan.unit / q.row_tiles;
+                rec.kv_head = plan.unit / row_tiles;
             }
             p.ws_records[blockIdx.x] = rec;
         }
@@ -1327,7 +1344,7 @@ __global__ void __launch_bounds__(kTreeRows) tree_merge_kernel(
     const int span = rec.parts <= kMergeFew || rec.rows > 64 ? 128 : rec.rows > 32 ? 64 : 32;
     const int row = threadIdx.x % span, grp = threadIdx.x / span, groups = kTreeRows / span;
     const auto slot = [&](int i) {
-        return i == 0 ? (size_t)(b - 1) * 2 + 1 : (size_t)(b + i - 1) * 2;
+        return i == 0 ? (size_t)(b - rec.stride) * 2 + 1 : (size_t)(b + (i - 1) * rec.stride) * 2;
     };
     constexpr int kChunk = 4; // parts whose loads are in flight together
     const int c0 = blockIdx.y * kMergeCols;

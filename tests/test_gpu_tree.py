@@ -725,3 +725,15 @@ def test_whole_step_in_one_graph(pk):
             res.append([x.clone() for x in (out, acc, lens, nxt, *keys, *values)])
         for x, y in zip(*res):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("cache,trees,group,dim", [
+    ("f16", [64, 50, 0, 33], 4, 64),     # two row tiles each (of 128 rows)
+    ("bf16", [120, 64, 100], 4, 128),    # four, two and four
+    ("fp8", [40, 64], 4, 128), ("f16", [64, 20], 4, 64), ("f16", [96, 64], 4, 64)])
+def test_tree_decode_row_tiles_in_pairs(pk, cache, trees, group, dim):
+    """Trees that all have an even number of row tiles, which two CTAs share,
+    and some of an odd number among them, split over many CTAs and not."""
+    for ctx in ([30, 400, 70, 1][:len(trees)], [9000, 3000, 5, 2500][:len(trees)]):
+        b = TreeBatch(28, ctx, trees, kv_heads=2, group=group, dim=dim, cache=cache)
+        b.check(b.decode(pk))
