@@ -544,7 +544,7 @@ def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, 
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     _call(_lib.pa_tree_decode, dev, out.data_ptr(), kind, query.data_ptr(), S, N, H,
           key_cache.data_ptr(), value_cache.data_ptr(), desc, block_tables.data_ptr(), width,
-          context_lens.data_ptr(), tree_start.data_ptr(), mask.data_ptr(), words, scale,
+          context_lens.data_ptr(), tree_start.data_ptr(), mask.data_ptr(), words, float(scale),
           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           _err_ptr(dev_err, dev))
     return out

@@ -737,3 +737,119 @@ def test_tree_decode_row_tiles_in_pairs(pk, cache, trees, group, dim):
     for ctx in ([30, 400, 70, 1][:len(trees)], [9000, 3000, 5, 2500][:len(trees)]):
         b = TreeBatch(28, ctx, trees, kv_heads=2, group=group, dim=dim, cache=cache)
         b.check(b.decode(pk))
+
+
+# --- the binding's refusals, and odd but allowed calls --------------------------------------------
+
+def test_binding_refuses_wrong_tensors(pk):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = TreeBatch(29, [20, 3], [4, 5])
+    q, k, v, table, ctx, start, mask = b.cuda(pk)
+    out, ws = torch.empty_like(q), pk.alloc_tree_workspace(k)
+    good = dict(out=out, query=q, key_cache=k, value_cache=v, block_tables=table,
+                context_lens=ctx, tree_start=start, mask=mask, scale=np.float32(0.125),
+                workspace=ws)
+    pk.tree_decode(**good)
+    for bad in (dict(out=out[:-1]), dict(out=out.double()), dict(out=out.transpose(0, 1)),
+                dict(query=q.bfloat16()), dict(query=q[..., :32]), dict(query=q.cpu()),
+                dict(query=q[:, ::2]), dict(value_cache=v[:-1]), dict(value_cache=v.bfloat16()),
+                dict(key_cache=k.transpose(1, 2)), dict(block_tables=table.long()),
+                dict(block_tables=table[0]), dict(block_tables=table[:1]),
+                dict(block_tables=table.t()), dict(context_lens=ctx[:1]),
+                dict(context_lens=ctx.long()), dict(tree_start=start[:2]),
+                dict(tree_start=start[:0]), dict(tree_start=start.cpu()), dict(mask=mask[1:]),
+                dict(mask=mask[:, 0]), dict(workspace=ws[:-16].cpu()),
+                dict(dev_err=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            pk.tree_decode(**{**good, **bad})
+    for bad in (dict(workspace=ws[:-16]), dict(workspace=ws[1:]),
+                dict(scale=float("nan"))):
+        with pytest.raises(pk.PagedKVError):
+            pk.tree_decode(**{**good, **bad})
+    par = torch.tensor([-1, 0, 0, 1], **i32)
+    st = torch.tensor([0, 4], **i32)
+    m, d = torch.zeros(4, 1, **i32), torch.zeros(4, **i32)
+    for args in ((m[:3], d, par, st), (m, d[:3], par, st), (m.long(), d, par, st),
+                 (m, d, par.long(), st), (m, d, par[::2], st), (m.t(), d, par, st),
+                 (m, d, par, st[:0]), (m, d, par[None], st), (m.cpu(), d, par, st)):
+        with pytest.raises(ValueError):
+            pk.tree_mask(*args)
+    tok = torch.zeros(4, dtype=torch.int64, device="cuda")
+    acc, ln, nx = torch.zeros(1, 3, **i32), torch.zeros(1, **i32), tok[:1].clone()
+    for args in ((acc[0], ln, nx, par, st, tok, tok), (acc, ln.long(), nx, par, st, tok, tok),
+                 (acc, ln, nx.int(), par, st, tok, tok), (acc, ln, nx, par, st, tok[:3], tok),
+                 (acc, ln, nx, par, st, tok, tok.int())):
+        with pytest.raises(ValueError):
+            pk.tree_accept(*args)
+    for kw in (dict(key_caches=[k, k[:-1]], value_caches=[v, v]),
+               dict(value_caches=[]), dict(key_caches=[k.float()]), dict(value_caches=[v.bfloat16()]),
+               dict(key_caches=[k.cpu()]), dict(accepted=acc[0]), dict(context_lens=ctx)):
+        call = dict(key_caches=[k], value_caches=[v], block_tables=table[:1], context_lens=ctx[:1],
+                    accepted=acc, accepted_lens=ln)
+        call.update(kw)
+        with pytest.raises(ValueError):
+            pk.tree_compact(**call)
+
+
+def test_calls_with_nothing_to_do(pk):
+    """No sequences; sequences with empty trees and no rows; no block columns."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none = torch.zeros(0, **i32)
+    tok = torch.zeros(0, dtype=torch.int64, device="cuda")
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.float16, device="cuda")
+    q = torch.zeros(0, 8, 64, dtype=torch.float16, device="cuda")
+    for S in (0, 3):
+        start = torch.zeros(S + 1, **i32)
+        ctx = torch.full((S,), 7, **i32)
+        pk.tree_mask(torch.zeros(0, 1, **i32), none, none, start)
+        acc, ln = torch.full((S, 4), 9, **i32), torch.full((S,), 9, **i32)
+        nx = torch.full((S,), 9, dtype=torch.int64, device="cuda")
+        pk.tree_accept(acc, ln, nx, none, start, tok, tok)
+        assert (acc == -1).all() and (ln == 0).all() and (nx == -1).all()
+        err = torch.zeros(1, **i32)
+        pk.tree_decode(q.clone(), q, k, k, torch.zeros(S, 1, **i32), ctx, start,
+                       torch.zeros(0, 1, **i32), 0.1, dev_err=err)
+        pk.tree_compact([k], [k.clone()], torch.zeros(S, 1, **i32), ctx, acc, ln, dev_err=err)
+        assert int(err.item()) == 0
+    # A tree, but no column in the table: NaN rows, as for any that does not fit.
+    out = torch.zeros(2, 8, 64, dtype=torch.float16, device="cuda")
+    err = torch.zeros(1, **i32)
+    pk.tree_decode(out, torch.zeros_like(out), k, k, torch.zeros(1, 0, **i32),
+                   torch.zeros(1, **i32), torch.tensor([0, 2], **i32), torch.zeros(2, 1, **i32), 0.1,
+                   dev_err=err)
+    assert int(err.item()) == pk.PA_DEVERR_CONTEXT_LEN and torch.isnan(out).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_tree_decode_drawn_cases(pk, seed):
+    """Shapes, lengths, masks and types drawn over their ranges."""
+    rng = np.random.default_rng(1000 + seed)
+    cache = ["f16", "bf16", "fp8"][seed % 3]
+    kv, group = [(1, 8), (2, 4), (8, 1), (5, 7), (1, 33), (3, 2), (2, 16), (1, 1)][seed % 8]
+    S = int(rng.integers(1, 7))
+    top = int(2 ** rng.uniform(0, 11.5))
+    ctx = [int(x) for x in rng.integers(0, top + 1, S)]
+    trees = [int(x) for x in rng.integers(0, int(2 ** rng.uniform(0, 7.5)) + 1, S)]
+    trees[0] = max(trees[0], 1)
+    b = TreeBatch(seed, ctx, trees, kv_heads=kv, group=group, dim=[64, 128][seed // 2 % 2],
+                  block=[8, 16, 32][seed // 3 % 3], cache=cache,
+                  io=["f16", "bf16"][seed // 6 % 2] if cache == "fp8" else None,
+                  masks=["tree", "any"][seed // 4 % 2], shape=["bushy", "chain"][seed // 5 % 2],
+                  pad=int(rng.integers(0, 4)), q_gain=float(2 ** rng.uniform(-2, 3)),
+                  words=None if seed % 2 else max(1, -(-max(trees) // 32)) + 1)
+    scale = b.scale * float(rng.choice([1.0, 1.0, -1.0]))
+    b.check(b.decode(pk, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+def test_tree_decode_fp8_scales_of_any_size(pk, io):
+    """Row scales from 2^-30 to 2^12 side by side, and rows of zeros."""
+    b = TreeBatch(30, [150, 3], [10, 7], kv_heads=2, group=4, dim=64, cache="fp8", io=io)
+    n = 16 * 64
+    rng = np.random.default_rng(5)
+    for which, (lo, hi) in ((0, (-3, 3)), (1, (-30, 12))):
+        sc = b.pools[which][..., n:].contiguous().view(torch.float32)
+        sc *= torch.from_numpy(2.0 ** rng.integers(lo, hi, sc.shape)).float()
+        sc[::3, :, ::5] *= 0
+        b.pools[which][..., n:] = sc.view(torch.uint8)
+    b.check(b.decode(pk, torch.float32))

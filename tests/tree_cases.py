@@ -148,9 +148,12 @@ class TreeBatch:
         a bound on each element's error before the output is rounded.
 
         The bound follows the stated precision. With A = sum_j p_j |v_j|:
-        rounding p to the row type is off by at most eps/2 of each term, so
-        eps/2 * A; p of fp16 rows below 2^-14 loses up to 2^-25 absolutely,
-        n * 2^-25 * max |v|; a score summed in fp32 is off by at most
+        rounding p to the row type (fp16 for fp8 caches) is off by at most
+        eps/2 of each term, so eps/2 * A; fp16 weights below 2^-14 lose up to
+        2^-25 absolutely, n * 2^-25 * max |v| (for fp8 caches, where p times
+        the row's scale over at most twice the largest scale is rounded, max
+        |v| is at least half of what a lost weight stands for, and weights
+        are 2^8 above p); a score summed in fp32 is off by at most
         (dim + 4) * 2^-24 * sum |q||k| * scale = d, which moves p by 2 d
         relatively; exp2 and the scale factor are good to 2^-20; and n terms
         summed in fp32, where a tensor core may truncate, are off by at most
@@ -159,7 +162,8 @@ class TreeBatch:
         out = torch.full((self.rows, self.heads, self.dim), float("nan"), dtype=torch.float64)
         room = torch.zeros_like(out)
         k_all, v_all = self.values(0), self.values(1)
-        eps = torch.finfo(self.io).eps / 2
+        weights = torch.float16 if self.cache == "fp8" else self.io
+        eps = torch.finfo(weights).eps / 2
         for s, t in enumerate(self.trees):
             a, n, c = int(self.start[s]), self.ctx[s] + t, self.ctx[s]
             if t == 0:
@@ -185,7 +189,7 @@ class TreeBatch:
                         d = (self.dim + 4) * 2.0 ** -24 * abs(scale) * \
                             (q[h][r].abs() @ kh[seen].abs().T).max()
                         sub = n * 2.0 ** -25 * vh[seen].abs().nan_to_num(0, 0, 0).max() \
-                            if self.io == torch.float16 else 0.0
+                            if weights == torch.float16 else 0.0
                         room[a + r, h] = mag * (eps + 2 * d + 2.0 ** -20 + n * 2.0 ** -23) + sub
         return out, room
 
