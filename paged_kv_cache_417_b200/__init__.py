@@ -513,18 +513,24 @@ def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, 
     ``out`` may be fp16, bf16 or fp32; ``workspace`` is allocated here when
     not given."""
     i32 = torch.int32
-    _need_cache(key_cache, "key_cache")
-    _need_cache(value_cache, "value_cache", key_cache)
-    desc, row = cache_desc(key_cache), io_dtype(key_cache)
     if isinstance(key_cache, Fp8Cache):
+        _need_cache(key_cache, "key_cache")
+        _need_cache(value_cache, "value_cache", key_cache)
+        desc, row = cache_desc(key_cache), key_cache.io_dtype
         dev = key_cache.data.get_device()
         if value_cache.io_dtype != row or value_cache.data.get_device() != dev or \
                 value_cache.block_size != key_cache.block_size:
             raise ValueError("value_cache does not match the other cache")
     else:
-        dev = key_cache.get_device()
-        if value_cache.get_device() != dev:
+        row = key_cache.dtype
+        if row not in (torch.float16, torch.bfloat16):
+            raise ValueError("cache dtype must be float16 or bfloat16")
+        shape, dev = _first(key_cache, "key_cache", row, 4)
+        if isinstance(value_cache, Fp8Cache):
             raise ValueError("value_cache does not match the other cache")
+        _sized(value_cache, "value_cache", row, dev, shape)
+        code = _DTYPE[row]
+        desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], code, code)
     (N, H, D), on = _first(query, "query", row, 3)
     if on != dev:
         raise ValueError(f"query is on {query.device}, not cuda:{dev}")
@@ -545,8 +551,7 @@ def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, 
     _call(_lib.pa_tree_decode, dev, out.data_ptr(), kind, query.data_ptr(), S, N, H,
           key_cache.data_ptr(), value_cache.data_ptr(), desc, block_tables.data_ptr(), width,
           context_lens.data_ptr(), tree_start.data_ptr(), mask.data_ptr(), words, float(scale),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          _err_ptr(dev_err, dev))
+          workspace.data_ptr(), workspace.nbytes, _err_ptr(dev_err, dev))
     return out
 
 
