@@ -342,7 +342,7 @@ const char *pa_status_string(pa_status s)
     return "unknown status";
 }
 
-int32_t pa_version(void) { return 100; }
+int32_t pa_version(void) { return 200; }
 
 pa_status pa_write_kv(const void *key, const void *value, int32_t num_tokens, int32_t num_heads,
                       const int64_t *slot_mapping, void *key_cache, void *value_cache,
