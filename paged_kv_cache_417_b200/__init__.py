@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import operator
 import os
 
@@ -503,6 +504,12 @@ def alloc_tree_workspace(cache):
                            device=cache.device)
 
 
+@functools.lru_cache(maxsize=64)
+def _desc_of(num_blocks, num_kv_heads, block_size, head_dim, code):
+    """The descriptor of a 16-bit cache of these sizes, which nothing changes."""
+    return CacheDesc(num_blocks, block_size, num_kv_heads, head_dim, code, code)
+
+
 def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, tree_start, mask,
                 scale, workspace=None, dev_err=None):
     """Attention of every node of every drafted tree: ``query`` and ``out``
@@ -530,7 +537,7 @@ def tree_decode(out, query, key_cache, value_cache, block_tables, context_lens, 
             raise ValueError("value_cache does not match the other cache")
         _sized(value_cache, "value_cache", row, dev, shape)
         code = _DTYPE[row]
-        desc = CacheDesc(shape[0], shape[2], shape[1], shape[3], code, code)
+        desc = _desc_of(*shape, code)
     (N, H, D), on = _first(query, "query", row, 3)
     if on != dev:
         raise ValueError(f"query is on {query.device}, not cuda:{dev}")
