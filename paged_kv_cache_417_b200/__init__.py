@@ -398,8 +398,9 @@ def swap_blocks(src_key_caches, src_value_caches, dst_key_caches, dst_value_cach
 # checks are written for speed: device indices instead of device objects, the
 # raw stream, no context manager unless the tensors are on another device than
 # the current one.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
