@@ -46,7 +46,7 @@
 // rows that see it one by one (rescue_rows).
 //
 // Measured (B200, unthrottled): 96 sequences of 128-2048 tokens, 16 nodes, 32
-// heads over 8, D 128, f16: 93 us, 6.1 TB/s while the pieces run, then 10 us
+// heads over 8, D 128, f16: 92 us, 6.1 TB/s while the pieces run, then 10 us
 // of uneven ends; 8 sequences of 16k-32k tokens, bf16: 150 us, 5.7 TB/s in
 // all; 64-node trees: 113 us, 706 TFLOP/s, bound by the chain from S to P of
 // a tile (about 2700 cycles, two CTAs overlapping). Under the power limit all
@@ -527,6 +527,10 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     int s = sh.plan.seq;
     TreeSeq q = sh.plan.q;
     const int stride = sh.plan.stride;
+    // Keys and values that one CTA reads once leave L2 to the partial results
+    // and query rows (33 sequences of 32 K/V heads 97 -> 94 us, the 8-head layer
+    // 94 -> 92, the others within 1 %); those that two CTAs share stay.
+    const uint64_t policy = l2_policy(stride == 1);
     int64_t unit_begin = sh.plan.unit_begin;
     int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
     // Widens tile `of` of the CTA, the first `blocks` blocks of which came.
@@ -712,7 +716,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                                  pool + (int64_t)from[b] * C::kBlockBytes, C::kBlockBytes, bar);
                     else
                         tma_load_4d(to + b * C::kBlockBytes, map, 0, 0, 0, from[b] * (BS / 8),
-                                    bar);
+                                    bar, policy);
                 }
             }
             __syncwarp();
