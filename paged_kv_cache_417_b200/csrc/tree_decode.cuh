@@ -337,7 +337,12 @@ template <int NS> struct TreeShared {
     int64_t sums[32];
     TreeSegment seg[4];
     int32_t poison[4];       // segment met a block id outside the pool
-    uint32_t strange[2];     // tokens of a tile whose V row holds NaN or infinity
+    // Tokens of a tile whose V row holds NaN or infinity, by the tile's parity:
+    // a warp that sets bits for tile it + 2 has met all others after tile it + 1
+    // set its own (sync_warps), which is after each of them has read tile it's.
+    // One buffer would let a warp with nothing else to do in a tile set the
+    // next one's bits before a late warp has read this one's.
+    uint32_t strange[2][2];
     // fp8 caches: raw tiles, and the row scales of four tiles.
     uint64_t raw_full[2][kRawStages], ks_full[4], vs_full[4];
     alignas(16) float ks[4][kTreeTile]; // times scale * log2(e)
@@ -847,7 +852,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
         mbar_init(smem_addr(&sh.drain), 1);
         fence_mbar_init();
         sh.keep_o = -1;
-        sh.strange[0] = sh.strange[1] = 0;
+        sh.strange[0][0] = sh.strange[0][1] = sh.strange[1][0] = sh.strange[1][1] = 0;
     }
     if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sh.tmem), C::kColumns);
@@ -1062,11 +1067,11 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                     }
                     if (bad)
-                        atomicOr(&sh.strange[vj >> 5], 1u << (vj & 31));
+                        atomicOr(&sh.strange[it & 1][vj >> 5], 1u << (vj & 31));
                     if (!sync_warps())
                         break;
-                    strange = (uint64_t)*(volatile uint32_t *)&sh.strange[1] << 32 |
-                              *(volatile uint32_t *)&sh.strange[0];
+                    strange = (uint64_t)*(volatile uint32_t *)&sh.strange[it & 1][1] << 32 |
+                              *(volatile uint32_t *)&sh.strange[it & 1][0];
                 }
                 constexpr int NC = kTreeTile;
                 uint32_t x[NC];
@@ -1231,7 +1236,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                                 "r"(0)
                                 : "memory");
                     if (tid < 2)
-                        *(volatile uint32_t *)&sh.strange[tid] = 0;
+                        *(volatile uint32_t *)&sh.strange[it & 1][tid] = 0;
                     fence_proxy_async_smem();
                     if (!sync_warps())
                         break;

@@ -853,3 +853,37 @@ def test_tree_decode_fp8_scales_of_any_size(pk, io):
         sc[::3, :, ::5] *= 0
         b.pools[which][..., n:] = sc.view(torch.uint8)
     b.check(b.decode(pk, torch.float32))
+
+
+@pytest.mark.parametrize("cache,io,dim", [("f16", "f16", 128), ("bf16", "bf16", 64),
+                                          ("fp8", "f16", 64), ("fp8", "bf16", 128)])
+def test_tree_decode_odd_rows_in_the_second_masked_tile_only(pk, cache, io, dim):
+    """Trees that cross a 64-token boundary, at most 64 rows each (two of the four
+    softmax warps idle): V is finite in their first masked tile, and holds NaN behind
+    the last token and an infinity in a node of the second one. Every call of many
+    gives the same bits."""
+    n = 60
+    b = TreeBatch(31, [50 + i % 14 + 64 * (i % 3) for i in range(n)], [16] * n, kv_heads=4,
+                  group=4, dim=dim, cache=cache, io=io)
+    for s in range(0, n, 4):
+        j = (b.ctx[s] + 15) // 64 * 64  # the first node of the second tile
+        assert b.ctx[s] < j < b.ctx[s] + 16
+        blk, off = int(b.table[s, j // 16]), j % 16
+        if cache == "fp8":
+            sc = b.pools[1][blk, :, 16 * dim:].contiguous().view(torch.float32)
+            sc[:, off] = float("inf")
+            b.pools[1][blk, :, 16 * dim:] = sc.view(torch.uint8)
+        else:
+            b.pools[1][blk, :, off, 5] = float("inf")
+    q, k, v, table, ctx, start, mask = b.cuda(pk)
+    ws = pk.alloc_tree_workspace(k)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.full_like(q, float("nan")) for _ in range(20)]
+    for _ in range(20):
+        for o in outs:
+            pk.tree_decode(o, q, k, v, table, ctx, start, mask, b.scale, workspace=ws, dev_err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        for o in outs[1:]:
+            assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+    b.check(outs[0])
