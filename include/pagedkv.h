@@ -372,9 +372,11 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
  * Precision: products and sums, the softmax and the P.V sums are fp32, the
  * weight p of the P.V products is rounded first, to the row type (fp8 caches:
  * p times the row's V scale over a power of two, to f16), and the output once,
- * to out_dtype. A block id outside the pool sets PA_DEVERR_BLOCK_ID and makes
- * that sequence's output NaN; a bounded wait that runs out, or lengths that
- * change under the call, sets PA_DEVERR_TIMEOUT and leaves rows unwritten.
+ * to out_dtype. Sums are of p times a factor of up to 2^14, so values of V
+ * beyond 2^114 over the number of tokens may overflow. A block id outside
+ * the pool sets PA_DEVERR_BLOCK_ID and makes that sequence's output NaN; a
+ * bounded wait that runs out, or lengths that change under the call, sets
+ * PA_DEVERR_TIMEOUT and leaves rows unwritten.
  */
 pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,
                          int32_t num_tokens, int32_t num_heads, const void *key_cache,

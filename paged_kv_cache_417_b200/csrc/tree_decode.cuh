@@ -83,6 +83,12 @@ constexpr int kRawStages = 2; // fp8 tiles on their way, of K and of V
 constexpr int kTreeUnitCost = 4;
 constexpr float kTreeSlack = 6.f;
 constexpr float kTreeBias = 8.f;
+// fp8 caches: bits of the least power of two that V scales are taken relative
+// to, 2^-104. p / R is formed in fp32 before a V scale comes in, up to
+// 2^(kTreeBias + kTreeSlack) / R, and 64 of them are summed: 2^124. Weights of
+// smaller scales lose bits in f16, 2^-25 of R / 2^kTreeBias at most, times a
+// code below 2^9: 2^-128 a token, under fp32's normal range.
+constexpr uint32_t kTreeLeastR = (127u - 104u) << 23;
 
 // Where a unit cut before CTA b's piece (and not earlier) has its parts: part
 // 0 in the second slot of the CTA with the piece before, parts 1 .. parts-1
@@ -1108,8 +1114,9 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         factor = 1.f;
                         // Weights are p * scale / R, R the power of two
-                        // above the largest V scale so far: in f16's range
-                        // whatever the scales. 1 / R goes into the exponent.
+                        // above the largest V scale so far, at least
+                        // kTreeLeastR: in f16's range. 1 / R goes into the
+                        // exponent.
                         float top_v = sh.vmax[it & 3];
                         if (kMasked) {
                             top_v = 0.f;
@@ -1124,8 +1131,9 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         if (top_v > R) {
                             const float up2 = __uint_as_float(
-                                min((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u,
-                                    0x7e800000u));
+                                max(min((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u,
+                                        0x7e800000u),
+                                    kTreeLeastR));
                             alpha = R / up2;
                             rescale = tile > d.tile0;
                             R = up2;
@@ -1259,7 +1267,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                 // minus infinity is NaN, as 0/0 is.
                 const bool none = l == 0.f && !saw;
                 if (d.slot < 0) {
-                    const float inv = none ? 0.f : C::kFp8 ? R / l : 1.f / l;
+                    const float inv = none ? 0.f : 1.f / l; // R / l could be subnormal
                     const size_t at =
                         ((size_t)(d.row0 + node) * p.num_heads + d.kv_head * p.group +
                          (tid - node * p.group)) * D;
@@ -1268,10 +1276,12 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         uint32_t o[32];
                         tmem_ld_x32(o_column + c0, o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
+                        for (int k = 0; k < 32; ++k) {
+                            const float x = __uint_as_float(o[k]) * inv;
                             o[k] = __float_as_uint(poison ? NAN
                                                    : none ? 0.f
-                                                          : __uint_as_float(o[k]) * inv);
+                                                          : C::kFp8 ? x * R : x);
+                        }
                         if (now_live)
                             store_row32(p.out, p.out_dtype, at + c0, o);
                         __syncwarp();

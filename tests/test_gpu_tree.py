@@ -887,3 +887,43 @@ def test_tree_decode_odd_rows_in_the_second_masked_tile_only(pk, cache, io, dim)
         for o in outs[1:]:
             assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
     b.check(outs[0])
+
+
+@pytest.mark.parametrize("io", ["f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("powers", ["tiny", "subnormal", "tiny_first", "huge", "huge_first", "any"])
+def test_tree_decode_fp8_extreme_value_scales(pk, io, dim, powers):
+    """V scales down to the smallest number and up to 2^94 or so: alone, in the first
+    64-token tile (and every later one ordinary, or the other way round), and mixed."""
+    ctx = [150, 3, 700]
+    b = TreeBatch(32, ctx, [10, 7, 9], kv_heads=2, group=4, dim=dim, cache="fp8", io=io)
+    n = 16 * dim
+    rng = np.random.default_rng(6)
+    sc = b.pools[1][..., n:].contiguous().view(torch.float32)  # about 2^-7 each
+    first = torch.zeros(sc.shape[0], dtype=torch.bool)
+    for s in range(3):
+        first[b.table[s, :4].long().clamp(min=0)] = True
+    first = first[:, None, None]
+    if powers == "tiny":
+        sc *= 2.0 ** -110
+    elif powers == "subnormal":
+        sc *= 2.0 ** -70
+        sc *= 2.0 ** -67
+    elif powers == "tiny_first":
+        sc = torch.where(first, sc * 2.0 ** -118, sc)
+    elif powers == "huge":
+        sc *= 2.0 ** 101
+    elif powers == "huge_first":
+        sc = torch.where(first, sc * 2.0 ** 101, sc * 2.0 ** -50)
+    else:
+        sc *= torch.from_numpy(2.0 ** rng.integers(-119, 101, sc.shape)).float()
+    b.pools[1][..., n:] = sc.view(torch.uint8)
+    got = b.decode(pk, torch.float32).double().cpu()
+    want, room = b.expected()
+    assert torch.isfinite(want).all() and torch.isfinite(got).all()
+    # Beside the bound of expected(): p times a scale over a power of two of at least
+    # 2^-104, times 2^8, is rounded to fp16, off by 2^-25 below its normal range; codes
+    # are at most 448 < 2^9. Rounding the output: half a step of fp32.
+    tokens = 709
+    lim = room + tokens * 2.0 ** (-25 - 8 - 104 + 9) + (want.abs() + room) * 2.0 ** -24 + 2.0 ** -150
+    assert ((got - want).abs() <= lim).all(), float(((got - want).abs() / lim).max())
