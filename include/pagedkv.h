@@ -376,7 +376,7 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
  * beyond 2^114 over the number of tokens may overflow. A block id outside
  * the pool sets PA_DEVERR_BLOCK_ID and makes that sequence's output NaN; a
  * bounded wait that runs out, or lengths that change under the call, sets
- * PA_DEVERR_TIMEOUT and leaves rows unwritten.
+ * PA_DEVERR_TIMEOUT and leaves rows unwritten or NaN.
  */
 pa_status pa_tree_decode(void *out, pa_dtype out_dtype, const void *query, int32_t num_seqs,
                          int32_t num_tokens, int32_t num_heads, const void *key_cache,

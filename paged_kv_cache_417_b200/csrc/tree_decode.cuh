@@ -868,6 +868,16 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
     tcgen05_fence_after();
     const uint32_t tmem = sh.tmem;
     bool ok = true;
+    // Parts that this CTA does not come to write (a wait that runs out, lengths
+    // that change under the call) must not be merged from what a call before
+    // left there: l = NaN makes rows of them NaN. The thread that fills a row
+    // later is the one that stores here.
+    if (tid < kTreeRows) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            __stcg(p.ws_ml + ((size_t)blockIdx.x * 2 + k) * kTreeRows + tid,
+                   make_float2(-INFINITY, NAN));
+    }
     const auto wait = [&](uint64_t &bar, uint32_t parity) {
         ok = ok && mbar_wait_suspended(smem_addr(&bar), parity, kWaitLimitNs);
         return ok;

@@ -927,3 +927,23 @@ def test_tree_decode_fp8_extreme_value_scales(pk, io, dim, powers):
     tokens = 709
     lim = room + tokens * 2.0 ** (-25 - 8 - 104 + 9) + (want.abs() + room) * 2.0 ** -24 + 2.0 ** -150
     assert ((got - want).abs() <= lim).all(), float(((got - want).abs() / lim).max())
+
+
+def test_tree_decode_workspace_keeps_nothing(pk):
+    """Every (m, l) pair of the workspace is this call's: rows that were not filled, as
+    after a wait that ran out, hold l = NaN, which makes what is merged from them NaN."""
+    b = TreeBatch(33, [5000, 20], [16, 5], kv_heads=2, dim=64)
+    q, k, *_ = b.cuda(pk)
+    ws = pk.alloc_tree_workspace(k)
+    old = 1.0
+    ws.view(torch.float32).fill_(old)
+    b.check(b.decode(pk, workspace=ws))
+    ctas = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    pairs = ws[-ctas * 2 * 128 * 8:]  # the workspace's last part
+    l = pairs.view(torch.float32).reshape(ctas, 2, 128, 2)[..., 1]
+    assert not (l == old).any()
+    assert torch.isnan(l).any() and torch.isfinite(l).any()
+    # One bad block in one part of a sequence that many CTAs share: NaN rows.
+    b.table[0, 100] = b.num_blocks
+    got = b.decode(pk, workspace=ws, want_err=pk.PA_DEVERR_BLOCK_ID)
+    assert torch.isnan(got[:16]).all() and torch.isfinite(got[16:]).all()
