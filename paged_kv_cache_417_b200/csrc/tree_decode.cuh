@@ -676,6 +676,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     int to_widen = 0, to_widen_left = 0; // blocks and tokens of the tile before
     uint32_t q_seen[2] = {0, 0}; // segments of each parity whose query rows were seen done
     bool was_whole = false;
+    int issued = 0, segs_issued = 0; // tiles and query rows whose copies were issued
     for (bool last = false; !last && ok; ++seg) {
         const int row_tiles = q.row_tiles >> (stride - 1); // this CTA's
         const int rt = unit % row_tiles * stride + sh.plan.lane, h = unit / row_tiles;
@@ -731,6 +732,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                 }
             }
             __syncwarp();
+            issued = it + 1;
             if constexpr (C::kFp8) {
                 if (it > 0)
                     widen(it - 1, to_widen, to_widen_left);
@@ -776,6 +778,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                                         0, h * p.group, d.row0 + b * (64 / p.group), u, qbar);
                 }
                 __syncwarp();
+                segs_issued = seg + 1;
             }
             id = next;
         }
@@ -802,14 +805,19 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     }
     if (C::kFp8 && ok)
         widen(it - 1, to_widen, to_widen_left);
-    if (!ok) { // let the copies in flight land before the CTA goes
+    if (!ok) {
+        // Let the copies in flight land before the CTA goes: those of the last
+        // kRing tiles issued, and of the last two segments' query rows (older
+        // ones were waited for before theirs could be overwritten). Waiting for
+        // a phase that was not begun would return at once with the one before
+        // it still open, so only what was issued counts.
         constexpr uint64_t kDrainNs = 10000000;
         constexpr int kRing = C::kFp8 ? kRawStages : NS;
-        for (int i = max(0, it - kRing + 1); i <= it; ++i)
+        for (int i = max(0, issued - kRing); i < issued; ++i)
             mbar_wait_bounded(smem_addr(C::kFp8 ? &sh.raw_full[is_v][i % kRing] : &full[i % kRing]),
                               (i / kRing) & 1, kDrainNs);
-        if (!is_v)
-            mbar_wait_bounded(smem_addr(&sh.q_full[seg & 3]), (seg >> 2) & 1, kDrainNs);
+        for (int i = max(0, segs_issued - 2); i < segs_issued; ++i)
+            mbar_wait_bounded(smem_addr(&sh.q_full[i & 3]), (i >> 2) & 1, kDrainNs);
     }
 }
 
