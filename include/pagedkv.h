@@ -418,7 +418,8 @@ pa_status pa_tree_accept(int32_t *accepted, int32_t *accepted_lens, int64_t *nex
  * both caches of every layer, in place.
  *
  * key_caches, value_caches  HOST arrays of num_layers device pointers, as for
- *                pa_copy_blocks.
+ *                pa_copy_blocks. A cache that stands in them more than once
+ *                (layers that share one) is moved once.
  * context_lens   device int32 [num_seqs], without the tree.
  * accepted, accepted_lens  device, as pa_tree_accept writes them: each path
  *                ascending. A length outside [0, max_path], a negative node

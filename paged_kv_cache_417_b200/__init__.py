@@ -590,7 +590,8 @@ def tree_compact(key_caches, value_caches, block_tables, context_lens, accepted,
                  dev_err=None):
     """Move the accepted nodes' K/V rows behind the context, in place and in
     every layer: position context_lens[s] + accepted[s, k] to position
-    context_lens[s] + k for k < accepted_lens[s]."""
+    context_lens[s] + k for k < accepted_lens[s]. A cache that layers share is
+    moved once."""
     L = len(key_caches)
     if len(value_caches) != L or not L:
         raise ValueError("need the same, non-zero number of K and V caches")

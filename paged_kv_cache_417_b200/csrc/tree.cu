@@ -340,8 +340,25 @@ pa_status pa_tree_compact(void *const *key_caches, void *const *value_caches,
             return fail(PA_ERR_INVALID_ARG, "NULL cache pointer for layer %d", l);
         if (!aligned16(key_caches[l]) || !aligned16(value_caches[l]))
             return fail(PA_ERR_INVALID_ARG, "cache of layer %d not 16-byte aligned", l);
-        p.key_caches[l] = key_caches[l];
-        p.value_caches[l] = value_caches[l];
+    }
+    // Layers may share a cache, or a layer K and V. Moves in place are not for
+    // doing twice (or by two CTAs at once), so each cache is taken once; a
+    // table of their addresses, at most half full, finds the repeated ones.
+    uint32_t mask = 3;
+    while (mask + 1 < 4u * num_layers)
+        mask = 2 * mask + 1;
+    const void *seen[4 * PA_MAX_LAYERS];
+    std::memset(seen, 0, (mask + 1) * sizeof(seen[0]));
+    int num_caches = 0;
+    for (int i = 0; i < 2 * num_layers; ++i) {
+        void *c = i < num_layers ? key_caches[i] : value_caches[i - num_layers];
+        uint32_t at = (uint32_t)(reinterpret_cast<uintptr_t>(c) >> 4) * 2654435761u >> 16 & mask;
+        while (seen[at] && seen[at] != c)
+            at = (at + 1) & mask;
+        if (!seen[at]) {
+            seen[at] = c;
+            p.caches[num_caches++] = c;
+        }
     }
     p.block_tables = block_tables;
     p.context_lens = context_lens;
@@ -356,7 +373,7 @@ pa_status pa_tree_compact(void *const *key_caches, void *const *value_caches,
     p.scaled = cache->dtype == PA_FP8_E4M3;
     p.row_vecs = cache->head_dim * (p.scaled ? 1 : 2) / 16;
     p.tile_bytes = (int32_t)tile_bytes(cache);
-    cudaError_t e = launch_pdl(tree_compact_kernel, dim3(num_seqs, num_layers, 2), dim3(128), 0,
+    cudaError_t e = launch_pdl(tree_compact_kernel, dim3(num_seqs, num_caches), dim3(128), 0,
                                static_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree_compact launch");

@@ -16,7 +16,7 @@
 // latency: one tree of 8 nodes 1.65 us, 256 of up to 255 nodes 2.1 us.
 //
 // tree_compact_kernel: row moves along the token axis only, so each
-// (layer, K or V, head, 16-byte column) is independent of all others: one
+// (cache, head, 16-byte column) is independent of all others: one
 // thread owns a column and moves it for every accepted node, in ascending
 // order, U loads before their stores. path[k] ascends, so path[k] >= k and a
 // store to slot k never hits a row that is still to be read: a later source
@@ -178,8 +178,7 @@ __global__ void __launch_bounds__(256) tree_accept_kernel(
 }
 
 struct CompactParams {
-    void *key_caches[PA_MAX_LAYERS];
-    void *value_caches[PA_MAX_LAYERS];
+    void *caches[2 * PA_MAX_LAYERS]; // K and V caches of all layers, each once
     const int32_t *block_tables, *context_lens, *accepted, *accepted_lens;
     int32_t *dev_err;
     int32_t num_blocks, block_size, num_heads, max_blocks_per_seq, max_path;
@@ -188,7 +187,7 @@ struct CompactParams {
     int32_t scaled;     // fp8: one fp32 scale per row behind the tile's codes
 };
 
-// Grid: (sequence, layer, K or V).
+// Grid: (sequence, cache).
 __global__ void __launch_bounds__(128) tree_compact_kernel(
     const __grid_constant__ CompactParams p)
 {
@@ -197,8 +196,8 @@ __global__ void __launch_bounds__(128) tree_compact_kernel(
     __shared__ uint8_t src_off[PA_TREE_MAX_NODES], dst_off[PA_TREE_MAX_NODES];
     pdl_launch_dependents();
     pdl_wait_prior_grid();
-    const int s = blockIdx.x, layer = blockIdx.y, which = blockIdx.z, tid = threadIdx.x;
-    const bool first = layer == 0 && which == 0;
+    const int s = blockIdx.x, tid = threadIdx.x;
+    const bool first = blockIdx.y == 0;
     const int n = p.accepted_lens[s], ctx = p.context_lens[s];
     if (n < 0 || n > p.max_path) {
         if (first && tid == 0)
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(128) tree_compact_kernel(
         report(p.dev_err, bad);
     if (__syncthreads_or(bad))
         return;
-    char *cache = static_cast<char *>(which ? p.value_caches[layer] : p.key_caches[layer]);
+    char *cache = static_cast<char *>(p.caches[blockIdx.y]);
     const int vecs = p.num_heads * p.row_vecs, columns = vecs + (p.scaled ? p.num_heads : 0);
     const int64_t block_bytes = (int64_t)p.num_heads * p.tile_bytes;
     constexpr int U = 4;

@@ -947,3 +947,25 @@ def test_tree_decode_workspace_keeps_nothing(pk):
     b.table[0, 100] = b.num_blocks
     got = b.decode(pk, workspace=ws, want_err=pk.PA_DEVERR_BLOCK_ID)
     assert torch.isnan(got[:16]).all() and torch.isfinite(got[16:]).all()
+
+
+@pytest.mark.parametrize("cache,layers", [("f16", 3), ("fp8", 3), ("bf16", 256)])
+def test_tree_compact_caches_that_layers_share(pk, cache, layers):
+    """A cache listed for several layers, or as K and V of one, is moved once."""
+    block, dim, heads = 16, 64, 2
+    pools = _pools(cache, 2, 8, heads, block, dim, 8)
+    table, ctx = [[2, 5, 1], [7, 0, 3]], [3, 14]
+    paths = [[0, 2, 3, 4, 7, 20], [1, 2, 3, 4, 5, 6, 7, 8]]
+    want = _moved(pools, cache, block, dim, table, ctx, paths)
+    acc = torch.tensor([p + [-1] * (8 - len(p)) for p in paths], dtype=torch.int32).cuda()
+    lens = torch.tensor([len(p) for p in paths], dtype=torch.int32).cuda()
+    wrap = (lambda x: pk.Fp8Cache(x, block, dim)) if cache == "fp8" else (lambda x: x)
+    a, b, c, d = map(wrap, pools)
+    keys, values = [a, b, a], [c, d, d]
+    if layers > 3:
+        keys, values = [a, b] * (layers // 2), [b, c] * (layers // 2 - 1) + [d, d]
+    pk.tree_compact(keys, values, torch.tensor(table, dtype=torch.int32).cuda(),
+                    torch.tensor(ctx, dtype=torch.int32).cuda(), acc, lens)
+    for x, y in zip(pools, want):
+        got = x.cpu() if cache == "fp8" else x.cpu().view(torch.int16)
+        assert torch.equal(got, y)
