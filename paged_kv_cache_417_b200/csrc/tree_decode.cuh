@@ -538,10 +538,12 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
     int s = sh.plan.seq;
     TreeSeq q = sh.plan.q;
     const int stride = sh.plan.stride;
-    // Keys and values that one CTA reads once leave L2 to the partial results
-    // and query rows (33 sequences of 32 K/V heads 97 -> 94 us, the 8-head layer
-    // 94 -> 92, the others within 1 %); those that two CTAs share stay.
-    const uint64_t policy = l2_policy(stride == 1);
+    // Keys and values that are read once leave L2 to the partial results and
+    // query rows (33 sequences of 32 K/V heads 97 -> 94 us, the 8-head layer 94
+    // -> 92); those of several row tiles stay for the tiles that follow (three
+    // tiles over 4 contexts of 32k, bf16: 273 -> 264 us; trees of one and two
+    // over 256-4096 tokens 112.0 -> 109.5).
+    uint64_t policy = l2_policy(q.row_tiles == 1);
     int64_t unit_begin = sh.plan.unit_begin;
     int unit = sh.plan.unit, tile = sh.plan.tile, it = 0, seg = 0;
     // Widens tile `of` of the CTA, the first `blocks` blocks of which came.
@@ -801,6 +803,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                 break;
             }
             q = tree_seq(p, s, BS);
+            policy = l2_policy(q.row_tiles == 1);
         }
     }
     if (C::kFp8 && ok)
