@@ -293,7 +293,6 @@ pa_status pa_bm_prepare_tree(pa_block_manager *bm, const int64_t *seqs, int32_t 
         (n > 0 && (!seqs || !tree_sizes || !block_tables || !context_lens || !copy_pairs)))
         return fail(PA_ERR_INVALID_ARG, "NULL pointer argument");
     // The whole step first, as for pa_bm_prepare_decode.
-    // Tables get the room they will need here, so nothing after this can throw.
     int64_t need = 0, nodes = 0;
     const int32_t bs = bm->block_size;
     try {
@@ -316,7 +315,6 @@ pa_status pa_bm_prepare_tree(pa_block_manager *bm, const int64_t *seqs, int32_t 
             if (after > max_blocks_per_seq || (int64_t)s->table.size() > max_blocks_per_seq)
                 return fail(PA_ERR_INVALID_ARG, "sequence %lld outgrows max_blocks_per_seq %d",
                             (long long)seqs[i], max_blocks_per_seq);
-            s->table.reserve((size_t)after);
             nodes += t;
             need += after - blocks_for(s->tokens, bs);
             if (t > 0 && s->tokens % bs != 0) {
@@ -337,6 +335,18 @@ pa_status pa_bm_prepare_tree(pa_block_manager *bm, const int64_t *seqs, int32_t 
     if ((size_t)need > bm->free_list.size())
         return fail(PA_ERR_INVALID_ARG, "pool exhausted: the step needs %lld blocks, %zu free",
                     (long long)need, bm->free_list.size());
+    // Tables get the room they will need (no more than the pool holds, by now),
+    // so nothing after this can throw.
+    try {
+        for (int32_t i = 0; i < n; ++i) {
+            pa_block_manager::Seq *s = bm->find(seqs[i]);
+            const size_t after = (size_t)blocks_for((int64_t)s->tokens + tree_sizes[i], bs);
+            if (after > s->table.capacity())
+                s->table.reserve(std::max(after, 2 * s->table.capacity()));
+        }
+    } catch (...) {
+        return fail(PA_ERR_INVALID_ARG, "out of host memory");
+    }
     int32_t pairs = 0, at = 0;
     tree_start[0] = 0;
     for (int32_t i = 0; i < n; ++i) {

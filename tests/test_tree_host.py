@@ -1,6 +1,7 @@
 """Drafted trees without a GPU: refusals before any launch, the block
 manager's share, and the plain forms the GPU tests compare with."""
 import ctypes
+import resource
 
 import numpy as np
 import pytest
@@ -195,6 +196,26 @@ def test_prepare_tree_refuses_without_change(pk):
     assert L.pa_bm_prepare_tree(None, None, 0, None, 1, None, None, None, None, None,
                                 None) == pk.PA_ERR_INVALID_ARG
     assert bm.prepare_tree([], [], 1)["tree_start"].tolist() == [0]
+
+
+def test_prepare_tree_refused_for_room_takes_no_memory(pk):
+    """A tree far beyond the pool is refused before its table gets any room."""
+    L = pk._lib
+    from paged_kv_cache_417_b200.block_manager import BlockManager
+
+    def mapped():
+        with open("/proc/self/statm") as f:
+            return int(f.read().split()[0]) * resource.getpagesize()
+    bm = BlockManager(4, 1)
+    bm.add_sequence(1)
+    seqs, sizes = np.array([1], dtype=np.int64), np.array([2 ** 29], dtype=np.int32)
+    room = [np.zeros(2, dtype=np.int64) for _ in range(5)]
+    before = mapped()
+    st = L.pa_bm_prepare_tree(bm._h, seqs.ctypes.data, 1, sizes.ctypes.data, 2 ** 30,
+                              *(x.ctypes.data for x in room), None)
+    assert st == pk.PA_ERR_INVALID_ARG and b"pool exhausted" in L.pa_last_error()
+    assert mapped() - before < 2 ** 28
+    assert bm.num_tokens(1) == 0 and bm.num_free == 4
 
 
 # --- the plain forms themselves ------------------------------------------------------------------
