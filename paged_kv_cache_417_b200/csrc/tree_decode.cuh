@@ -83,12 +83,13 @@ constexpr int kRawStages = 2; // fp8 tiles on their way, of K and of V
 constexpr int kTreeUnitCost = 4;
 constexpr float kTreeSlack = 6.f;
 constexpr float kTreeBias = 8.f;
-// fp8 caches: bits of the least power of two that V scales are taken relative
-// to, 2^-104. p / R is formed in fp32 before a V scale comes in, up to
+// fp8 caches: the least power of two R that V scales are taken relative to.
+// p / R is formed in fp32 before a V scale comes in, up to
 // 2^(kTreeBias + kTreeSlack) / R, and 64 of them are summed: 2^124. Weights of
 // smaller scales lose bits in f16, 2^-25 of R / 2^kTreeBias at most, times a
-// code below 2^9: 2^-128 a token, under fp32's normal range.
-constexpr uint32_t kTreeLeastR = (127u - 104u) << 23;
+// code below 2^9: 2^-128 a token, under fp32's normal range. (R / l is normal
+// for l up to 2^22, then loses a bit a doubling.)
+constexpr float kTreeLeastR = 0x1p-104f;
 
 // Where a unit cut before CTA b's piece (and not earlier) has its parts: part
 // 0 in the second slot of the CTA with the piece before, parts 1 .. parts-1
@@ -1053,7 +1054,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
             d = d_next;
             const bool warp_live = warp * 32 < d.rows, now_live = live;
             float m = -INFINITY, l = 0.f;
-            float R = 0.f; // fp8: a power of two, O is in units of
+            float R = kTreeLeastR; // fp8: a power of two, O is in units of
             bool saw = false, poison = false;
             for (int tile = d.tile0; tile < d.tile1 && ok; ++tile, ++it) {
                 const uint32_t s_column = tmem + lanes + C::kS0 + (it & 1) * kTreeTile;
@@ -1115,7 +1116,6 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                     for (int k = 0; k < NC; k += 32)
                         tmem_ld_x32(s_column + k, x + k);
                     float factor = c, log2_R = 0.f;
-                    [[maybe_unused]] float unit_R = 1.f;
                     if constexpr (C::kFp8) {
                         const float4 *ks = reinterpret_cast<const float4 *>(sh.ks[it & 3]);
 #pragma unroll
@@ -1152,16 +1152,13 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         if (top_v > R) {
                             const float up2 = __uint_as_float(
-                                max(min((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u,
-                                        0x7e800000u),
-                                    kTreeLeastR));
+                                min((__float_as_uint(top_v) + 0x7fffffu) & 0x7f800000u,
+                                    0x7e800000u));
                             alpha = R / up2;
                             rescale = tile > d.tile0;
                             R = up2;
                         }
-                        const int e = (int)(__float_as_uint(R) >> 23); // 0: only zero scales yet
-                        log2_R = e ? (float)(e - 127) : 0.f;
-                        unit_R = e ? R : 1.f;
+                        log2_R = (float)((int)(__float_as_uint(R) >> 23) - 127);
                     }
                     if (kMasked) {
 #pragma unroll
@@ -1209,7 +1206,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                     }
                     sum[0] = add_f32x2(sum[0], sum[1]);
                     const float more = sum[0].x + sum[0].y;
-                    l = fmaf(l, keep, C::kFp8 ? more * unit_R : more);
+                    l = fmaf(l, keep, C::kFp8 ? more * R : more);
                 };
                 if (warp_live) {
                     if (special)
@@ -1288,7 +1285,7 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                 // minus infinity is NaN, as 0/0 is.
                 const bool none = l == 0.f && !saw;
                 if (d.slot < 0) {
-                    const float inv = none ? 0.f : 1.f / l; // R / l could be subnormal
+                    const float inv = none ? 0.f : C::kFp8 ? R / l : 1.f / l;
                     const size_t at =
                         ((size_t)(d.row0 + node) * p.num_heads + d.kv_head * p.group +
                          (tid - node * p.group)) * D;
@@ -1297,12 +1294,10 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         uint32_t o[32];
                         tmem_ld_x32(o_column + c0, o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float x = __uint_as_float(o[k]) * inv;
+                        for (int k = 0; k < 32; ++k)
                             o[k] = __float_as_uint(poison ? NAN
                                                    : none ? 0.f
-                                                          : C::kFp8 ? x * R : x);
-                        }
+                                                          : __uint_as_float(o[k]) * inv);
                         if (now_live)
                             store_row32(p.out, p.out_dtype, at + c0, o);
                         __syncwarp();
