@@ -354,7 +354,7 @@ template <int NS> struct TreeShared {
     uint64_t raw_full[2][kRawStages], ks_full[4], vs_full[4];
     alignas(16) float ks[4][kTreeTile]; // times scale * log2(e)
     alignas(16) float vs[4][kTreeTile];
-    float vmax[4]; // the largest finite V scale of a tile that every row sees
+    float vmax[4]; // the largest finite V scale in size of a tile that every row sees
     uint32_t tmem;
     int32_t keep_o;          // tile whose P V adds to O although it is a segment's first
 };
@@ -573,7 +573,7 @@ __device__ __forceinline__ void tree_fetch(const TreeTmaParams &g, const bool is
                         x = j < left ? x : 0.f;
                         const bool fine = fabsf(x) < INFINITY;
                         odd[k] = __ballot_sync(0xffffffffu, !fine);
-                        top = fine ? fmaxf(top, x) : top;
+                        top = fine ? fmaxf(top, fabsf(x)) : top;
                         scales[j] = fine ? x : 1.f;
                     } else {
                         scales[j] = x * p.qk_scale_log2;
@@ -1135,9 +1135,9 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                         }
                         factor = 1.f;
                         // Weights are p * scale / R, R the power of two
-                        // above the largest V scale so far, at least
-                        // kTreeLeastR: in f16's range. 1 / R goes into the
-                        // exponent.
+                        // above the largest size of a V scale so far, at
+                        // least kTreeLeastR: in f16's range. 1 / R goes into
+                        // the exponent.
                         float top_v = sh.vmax[it & 3];
                         if (kMasked) {
                             top_v = 0.f;
@@ -1146,8 +1146,10 @@ __global__ void __launch_bounds__(TreeCfg<T, D, BS>::kThreads, kTreeCtasPerSm)
                                 const float4 v =
                                     *reinterpret_cast<const float4 *>(&sh.vs[it & 3][k]);
                                 const uint32_t b = (uint32_t)(seen >> k);
-                                top_v = max3(top_v, b & 1 ? v.x : 0.f, b & 2 ? v.y : 0.f);
-                                top_v = max3(top_v, b & 4 ? v.z : 0.f, b & 8 ? v.w : 0.f);
+                                top_v = max3(top_v, fabsf(b & 1 ? v.x : 0.f),
+                                             fabsf(b & 2 ? v.y : 0.f));
+                                top_v = max3(top_v, fabsf(b & 4 ? v.z : 0.f),
+                                             fabsf(b & 8 ? v.w : 0.f));
                             }
                         }
                         if (top_v > R) {

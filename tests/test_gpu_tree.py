@@ -969,3 +969,21 @@ def test_tree_compact_caches_that_layers_share(pk, cache, layers):
     for x, y in zip(pools, want):
         got = x.cpu() if cache == "fp8" else x.cpu().view(torch.int16)
         assert torch.equal(got, y)
+
+
+@pytest.mark.parametrize("dim,sign", [(64, "all"), (128, "all"), (64, "some"), (128, "some")])
+def test_tree_decode_fp8_negative_scales(pk, dim, sign):
+    """A row's values are its codes times its scale, whatever the scale's sign."""
+    b = TreeBatch(34, [150, 3, 70], [10, 7, 9], kv_heads=2, group=4, dim=dim, cache="fp8")
+    n = 16 * dim
+    rng = np.random.default_rng(7)
+    for which in (0, 1):
+        sc = b.pools[which][..., n:].contiguous().view(torch.float32)
+        if sign == "all":
+            sc *= -1
+        else:
+            # The negative ones are the larger in size.
+            neg = torch.from_numpy(rng.random(sc.shape) < 0.3)
+            sc = torch.where(neg, -sc * (16 if which else 1), sc / (16 if which else 1))
+        b.pools[which][..., n:] = sc.view(torch.uint8)
+    b.check(b.decode(pk, torch.float32))
