@@ -370,9 +370,10 @@ size_t pa_tree_decode_workspace_size(const pa_cache_desc *cache);
  * Nothing about the lengths is needed on the host: the work is divided on
  * the device, so a captured call can be replayed with other lengths.
  * Precision: products and sums, the softmax and the P.V sums are fp32, the
- * weight p of the P.V products is rounded first, to the row type (fp8 caches:
- * p times the row's V scale over a power of two, to f16), and the output once,
- * to out_dtype. Sums are of p times a factor of up to 2^14, so values of V
+ * weight p of the P.V products is rounded first, to the row type (to 8 bits
+ * with bf16 rows, where pa_decode keeps about 16; fp8 caches: p times the
+ * row's V scale over a power of two, to f16), and the output once, to
+ * out_dtype. Sums are of p times a factor of up to 2^14, so values of V
  * beyond 2^114 over the number of tokens may overflow. A block id outside
  * the pool sets PA_DEVERR_BLOCK_ID and makes that sequence's output NaN; a
  * bounded wait that runs out, or lengths that change under the call, sets

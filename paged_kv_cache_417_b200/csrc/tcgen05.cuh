@@ -76,9 +76,7 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// True in one lane of a converged warp, in a form the compiler knows to be so
-// (tcgen05 instructions take their operands from uniform registers; behind a
-// plain lane == 0 it emits a loop over lanes around each of them).
+// True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t one;

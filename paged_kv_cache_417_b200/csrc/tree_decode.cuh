@@ -45,12 +45,23 @@
 // infinity is zeroed in shared memory and, if it is a node's, added to the
 // rows that see it one by one (rescue_rows).
 //
-// Measured (B200, unthrottled): 96 sequences of 128-2048 tokens, 16 nodes, 32
-// heads over 8, D 128, f16: 92 us, 6.1 TB/s while the pieces run, then 10 us
-// of uneven ends; 8 sequences of 16k-32k tokens, bf16: 150 us, 5.7 TB/s in
-// all; 64-node trees: 113 us, 706 TFLOP/s, bound by the chain from S to P of
-// a tile (about 2700 cycles, two CTAs overlapping). Under the power limit all
-// of them run 8-15 % longer.
+// Precision of the weights. P has 16 bits: f16 for f16 rows and fp8 caches, 11
+// bits of each weight; bf16 for bf16 rows, 8 bits, where the one-token decode
+// multiplies a bf16 head and a bf16 remainder (16 bits). A second product a
+// tile would do the same here, for more work on the chain from S to P, which
+// bounds larger trees (not measured). Weights' errors are independent, so they add to the rounding
+// of a 16-bit output about once more of the same size: against 64 bits the
+// error is 1.4 times that of fp32 weights (8 contexts of 16k-32k tokens, bf16:
+// 2.3e-3 of the output's size, 1.7e-3; f16: 2.9e-4, 2.1e-4).
+//
+// Measured (B200), in bursts of 200 calls / in a steady loop, where the power
+// limit holds: 96 sequences of 128-2048 tokens, 16 nodes, 32 heads over 8, D
+// 128, f16: 91 / 106 us, HBM (5 TB/s in all, 6.1 while the pieces run) and
+// uneven ends of the pieces; 33 such sequences, 32 K/V heads: 93 / 111 us; 8
+// sequences of 16k-32k tokens, bf16: 152 / 182 us, HBM; 64-node trees: 113 / 137
+// us, 706 / 581 TFLOP/s, the chain from S to P of a tile (about 2700 cycles, two
+// CTAs overlapping); fp8 with bf16 rows, 64 sequences: 103 / 103 us, the
+// widening of codes.
 //
 // Layouts. K and V blocks lie in shared memory as [8-row group][64-element
 // half][8 rows][128 bytes], swizzled, which one 4-D box per block fetches
@@ -78,8 +89,12 @@ constexpr int kTreeCtasPerSm = 2;
 constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kFetchKWarp = 6, kFetchVWarp = 7, kTreeWarps = 8;
 constexpr int kRawStages = 2; // fp8 tiles on their way, of K and of V
 // Tiles of time that a unit costs beside its own (measured: 3.9 us for a unit
-// of one tile, 1.4 us for each further one). 96 sequences of 128-2048 tokens,
-// 8 K/V heads: 104 us at 1, 99 at 2, 94 at 4 and at 6.
+// of one tile, 1.4 us for each further one). us at 2, 4, 6 and 8: 96 sequences
+// of 128-2048 tokens, 8 K/V heads, D 128, f16 94.4, 92.6, 93.4, 94.6; fp8 with
+// bf16 rows 105.1, 104.0, 105.9, 106.3; 64-node trees 121.5, 116.5, 116.1,
+// 116.0; 32 K/V heads 96.2, 94.7, 95.8, 96.2. At D 64 2 is better (f16 69.8,
+// 71.5, 73.9, 76.5, fp8 with f16 rows 77.6, 78.6, 80.6, 81.4), by 1-4 %: one
+// value for all.
 constexpr int kTreeUnitCost = 4;
 constexpr float kTreeSlack = 6.f;
 constexpr float kTreeBias = 8.f;

@@ -23,8 +23,8 @@
 // path[k'] > path[k] >= k. No barrier and no staging is needed. Bound by HBM
 // for large batches, by its chain of dependent loads (length, path, table
 // entry, row) for small ones: 64 sequences, 4 rows each of 2 KB (8 heads x
-// 128, f16) in K and V of 32 layers (67 MB read and written) 9.3 us, one
-// sequence in one layer 2.4 us.
+// 128, f16) in K and V of 32 layers (67 MB read and written, in part in L2)
+// 9.1 us, the same of an fp8 cache 8.2 us, one sequence in one layer 2.4 us.
 #pragma once
 
 #include <climits>
